@@ -7,6 +7,8 @@ seeded synthetic input generators.
 
 from .binding import (  # noqa: F401
     Fp8bsError,
+    fp8_add_rmsnorm_quant,
+    fp8_add_rmsnorm_quant_ue8m0,
     fp8_block_gemm,
     fp8_block_gemm_quant,
     fp8_block_gemm_ue8m0,
@@ -16,6 +18,8 @@ from .binding import (  # noqa: F401
     fp8_grouped_gemm,
     fp8_grouped_gemm_ue8m0,
     fp8_linear,
+    fp8_moe_mlp,
+    fp8_moe_mlp_ue8m0,
     fp8_quant_act_group128_ue8m0,
     fp8_quant_weight_block128_ue8m0,
     fp8_quant_act_group128,
@@ -24,6 +28,8 @@ from .binding import (  # noqa: F401
     gemm_workspace_bytes,
     get_device_error,
     lib,
+    moe_route_topk,
+    moe_workspace_bytes,
     prune24_compress,
     set_wait_limit,
 )

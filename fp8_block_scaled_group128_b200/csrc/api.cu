@@ -384,6 +384,139 @@ int fp8_gather_columns(const void* src_bf16, int64_t P, int64_t M, int64_t Np, v
                                              static_cast<cudaStream_t>(stream)));
 }
 
+static int add_rmsnorm_quant(const void* x, const void* res, const void* w, float eps, int64_t M,
+                             int64_t K, void* res_out, void* y, void* q, void* s, bool ue8m0,
+                             void* stream) {
+  if (M < 0 || M > kMaxDim || K > kNormMaxK) return FP8BS_ERR_SHAPE;
+  if (int st = check_k(K)) return st;
+  if (!(eps >= 0.0f) || eps > 3.402823466e38f) return FP8BS_ERR_SHAPE;
+  if (M == 0) return FP8BS_OK;
+  if (!x || !q || !s) return FP8BS_ERR_NULL;
+  // a NULL pointer is aligned
+  if (!aligned16(x) || !aligned16(res) || !aligned16(w) || !aligned16(res_out) || !aligned16(y) ||
+      !aligned16(q) || (!ue8m0 && !aligned4(s)))
+    return FP8BS_ERR_ALIGN;
+  DeviceInfo dev;
+  if (int st = current_device_info(&dev)) return st;
+  return from_cuda(launch_add_rmsnorm_quant(x, res, w, eps, M, K, res_out, y, q, s, ue8m0,
+                                            static_cast<cudaStream_t>(stream)));
+}
+
+int fp8_add_rmsnorm_quant(const void* x_bf16, const void* residual_bf16, const void* weight_bf16,
+                          float eps, int64_t M, int64_t K, void* residual_out_bf16, void* y_bf16,
+                          void* q_e4m3, float* s, void* stream) {
+  return add_rmsnorm_quant(x_bf16, residual_bf16, weight_bf16, eps, M, K, residual_out_bf16,
+                           y_bf16, q_e4m3, s, false, stream);
+}
+
+int fp8_add_rmsnorm_quant_ue8m0(const void* x_bf16, const void* residual_bf16,
+                                const void* weight_bf16, float eps, int64_t M, int64_t K,
+                                void* residual_out_bf16, void* y_bf16, void* q_e4m3,
+                                uint8_t* s_ue8m0, void* stream) {
+  return add_rmsnorm_quant(x_bf16, residual_bf16, weight_bf16, eps, M, K, residual_out_bf16,
+                           y_bf16, q_e4m3, s_ue8m0, true, stream);
+}
+
+int moe_route_topk(const void* logits, int logits_bf16, const float* bias, int scoring, int64_t M,
+                   int64_t E, int64_t top_k, int64_t n_group, int64_t topk_group, int renormalize,
+                   float scale, int32_t* ids, float* weights, void* stream) {
+  if (M < 0 || M > kMaxDim || E < 1 || E > kMoeMaxE || top_k < 1 || top_k > E ||
+      top_k > kMoeMaxTopK)
+    return FP8BS_ERR_SHAPE;
+  if (scoring != FP8BS_ROUTE_SOFTMAX && scoring != FP8BS_ROUTE_SIGMOID) return FP8BS_ERR_SHAPE;
+  if (n_group < 1 || n_group > 32 || E % n_group != 0 || topk_group < 1 || topk_group > n_group ||
+      top_k > topk_group * (E / n_group))
+    return FP8BS_ERR_SHAPE;
+  if ((bias != nullptr || n_group > 1) && scoring != FP8BS_ROUTE_SIGMOID) return FP8BS_ERR_SHAPE;
+  if (M == 0) return FP8BS_OK;
+  if (!logits || !ids || !weights) return FP8BS_ERR_NULL;
+  if ((reinterpret_cast<uintptr_t>(logits) & (logits_bf16 ? 1u : 3u)) != 0 || !aligned4(bias) ||
+      !aligned4(ids) || !aligned4(weights))
+    return FP8BS_ERR_ALIGN;
+  DeviceInfo dev;
+  if (int st = current_device_info(&dev)) return st;
+  return from_cuda(launch_moe_route(logits, logits_bf16 != 0, bias,
+                                    scoring == FP8BS_ROUTE_SIGMOID, M, E, top_k, n_group,
+                                    topk_group, renormalize != 0, scale, ids, weights,
+                                    static_cast<cudaStream_t>(stream)));
+}
+
+static int check_moe_shape(int64_t M, int64_t K, int64_t I, int64_t E, int64_t top_k) {
+  if (M < 0 || M > kMoeMaxM || E < 1 || E > kMoeMaxE || top_k < 1 || top_k > kMoeMaxTopK)
+    return FP8BS_ERR_SHAPE;
+  if (int st = check_k(K)) return st;
+  if (int st = check_k(I)) return st;
+  // weight rows are 32-bit coordinates: E x 2I of gate+up, E x K of down
+  if (K > kMaxDim || I > kMaxDim / 2 || 2 * I > kMaxDim / E || K > kMaxDim / E)
+    return FP8BS_ERR_SHAPE;
+  return FP8BS_OK;
+}
+
+size_t fp8bs_moe_workspace_bytes(int64_t M, int64_t K, int64_t I, int64_t E, int64_t top_k) {
+  if (check_moe_shape(M, K, I, E, top_k) != FP8BS_OK || M == 0) return 0;
+  return moe_workspace_bytes(M, K, I, E, top_k);
+}
+
+static int moe_mlp(const void* qa, const void* sa, const int32_t* ids, const float* weights,
+                   const void* qg, const void* sg, const void* qd, const void* sd, void* y,
+                   int64_t M, int64_t K, int64_t I, int64_t E, int64_t top_k,
+                   int64_t first_expert, void* workspace, size_t workspace_bytes, bool ue8m0,
+                   void* stream) {
+  if (int st = check_moe_shape(M, K, I, E, top_k)) return st;
+  if (first_expert < 0 || first_expert > kMaxDim) return FP8BS_ERR_SHAPE;
+  if (M == 0) return FP8BS_OK;
+  if (!qa || !sa || !ids || !weights || !qg || !sg || !qd || !sd || !y) return FP8BS_ERR_NULL;
+  if (!aligned16(qa) || !aligned4(ids) || !aligned4(weights) || !aligned16(qg) ||
+      !aligned16(qd) || !aligned16(y) ||
+      (!ue8m0 && (!aligned4(sa) || !aligned4(sg) || !aligned4(sd))))
+    return FP8BS_ERR_ALIGN;
+  if (workspace == nullptr || !aligned16(workspace) ||
+      workspace_bytes < moe_workspace_bytes(M, K, I, E, top_k))
+    return FP8BS_ERR_WORKSPACE;
+  int* err = device_error_word();
+  if (err == nullptr) return FP8BS_ERR_CUDA;
+  MoeArgs a{};
+  a.qa = static_cast<const uint8_t*>(qa);
+  a.sa = sa;
+  a.ids = ids;
+  a.weights = weights;
+  a.qg = static_cast<const uint8_t*>(qg);
+  a.sg = sg;
+  a.qd = static_cast<const uint8_t*>(qd);
+  a.sd = sd;
+  a.y = static_cast<__nv_bfloat16*>(y);
+  a.M = static_cast<int>(M);
+  a.K = static_cast<int>(K);
+  a.I = static_cast<int>(I);
+  a.E = static_cast<int>(E);
+  a.top_k = static_cast<int>(top_k);
+  a.first_expert = static_cast<int>(first_expert);
+  a.workspace = workspace;
+  a.wait_limit = wait_limit();
+  a.err = err;
+  return launch_moe_mlp(a, ue8m0, static_cast<cudaStream_t>(stream));
+}
+
+int fp8_moe_mlp(const void* qa, const float* sa, const int32_t* ids, const float* weights,
+                const void* qw_gate_up, const float* sw_gate_up, const void* qw_down,
+                const float* sw_down, void* y_bf16, int64_t M, int64_t K, int64_t I, int64_t E,
+                int64_t top_k, int64_t first_expert, void* workspace, size_t workspace_bytes,
+                void* stream) {
+  return moe_mlp(qa, sa, ids, weights, qw_gate_up, sw_gate_up, qw_down, sw_down, y_bf16, M, K, I,
+                 E, top_k, first_expert, workspace, workspace_bytes, false, stream);
+}
+
+int fp8_moe_mlp_ue8m0(const void* qa, const uint8_t* sa_ue8m0, const int32_t* ids,
+                      const float* weights, const void* qw_gate_up,
+                      const uint8_t* sw_gate_up_ue8m0, const void* qw_down,
+                      const uint8_t* sw_down_ue8m0, void* y_bf16, int64_t M, int64_t K, int64_t I,
+                      int64_t E, int64_t top_k, int64_t first_expert, void* workspace,
+                      size_t workspace_bytes, void* stream) {
+  return moe_mlp(qa, sa_ue8m0, ids, weights, qw_gate_up, sw_gate_up_ue8m0, qw_down,
+                 sw_down_ue8m0, y_bf16, M, K, I, E, top_k, first_expert, workspace,
+                 workspace_bytes, true, stream);
+}
+
 int fp8bs_get_device_error(void* stream) {
   if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess)
     return FP8BS_ERR_CUDA;

@@ -239,6 +239,51 @@ __device__ __forceinline__ uint2 encode8_pow2(const uint4 v, float inv_scale) {
                     prmt(pow2_codes2(v.z, r2), pow2_codes2(v.w, r2), 0x5410u));
 }
 
+// Codes of fp32 values (the fused norm's and SwiGLU's outputs before any
+// rounding to bf16): e4m3(x / s) of 8 values against one scale. The quotients
+// take the same steps as for bf16 values (ScaleDivider); the code of an fp32 x
+// differs from that of the IEEE quotient at most where the quotient is within
+// an fp32 ulp of an E4M3 rounding boundary.
+__device__ __forceinline__ uint32_t codes4f(float x0, float x1, float x2, float x3,
+                                            const ScaleDivider& d) {
+  float q0, q1, q2, q3;
+  if (d.fast_all) {
+    d.neg_quotient2_unchecked(x0, x1, q0, q1);
+    d.neg_quotient2_unchecked(x2, x3, q2, q3);
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(q0, q1), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(q2, q3), __NV_SATFINITE, __NV_E4M3);
+    return prmt(lo, hi, 0x5410u) ^ 0x80808080u;
+  }
+  const bool zero = d.s == 0.0f;   // an all-zero group: the elements' signed zeros
+  q0 = zero ? x0 : d(x0);
+  q1 = zero ? x1 : d(x1);
+  q2 = zero ? x2 : d(x2);
+  q3 = zero ? x3 : d(x3);
+  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(q0, q1), __NV_SATFINITE, __NV_E4M3);
+  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(q2, q3), __NV_SATFINITE, __NV_E4M3);
+  return prmt(lo, hi, 0x5410u);
+}
+
+__device__ __forceinline__ uint2 encode8f(const float (&x)[8], const ScaleDivider& d) {
+  return make_uint2(codes4f(x[0], x[1], x[2], x[3], d), codes4f(x[4], x[5], x[6], x[7], d));
+}
+
+// The same against a power-of-two scale (the product is exact unless it
+// underflows).
+__device__ __forceinline__ uint32_t codes4f_pow2(float x0, float x1, float x2, float x3,
+                                                 float inv) {
+  const uint32_t lo =
+      __nv_cvt_float2_to_fp8x2(make_float2(x0 * inv, x1 * inv), __NV_SATFINITE, __NV_E4M3);
+  const uint32_t hi =
+      __nv_cvt_float2_to_fp8x2(make_float2(x2 * inv, x3 * inv), __NV_SATFINITE, __NV_E4M3);
+  return prmt(lo, hi, 0x5410u);
+}
+
+__device__ __forceinline__ uint2 encode8f_pow2(const float (&x)[8], float inv) {
+  return make_uint2(codes4f_pow2(x[0], x[1], x[2], x[3], inv),
+                    codes4f_pow2(x[4], x[5], x[6], x[7], inv));
+}
+
 // silu(g) = g * sigmoid(g) = g / (1 + e^-g) in fp32 with the fast exponential
 // and divide (relative error below 1e-6); the exponent's argument is clamped
 // at 80 so that 1 + e^-g stays finite (for g < -80 the result is then about

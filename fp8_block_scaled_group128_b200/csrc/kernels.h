@@ -4,6 +4,7 @@
 #include <cstddef>
 #include <cstdint>
 #include <cuda_runtime.h>
+#include <cuda_bf16.h>
 
 namespace fp8bs {
 
@@ -76,6 +77,42 @@ int launch_block_gemm(const void* qa, const float* sa, const void* qw, const flo
 int launch_sparse24_gemm(const void* qa, const float* sa, const void* vals, const uint8_t* meta,
                          const float* sw, void* y, int64_t M, int64_t N, int64_t K,
                          long long wait_limit, int* err, cudaStream_t stream);
+
+// Residual addition, RMS norm and 1x128 quantization (fp32 scales, or UE8M0
+// codes): res, w, res_out and y may be null; res_out may equal x or res.
+constexpr int64_t kNormMaxK = 65536;
+cudaError_t launch_add_rmsnorm_quant(const void* x, const void* res, const void* w, float eps,
+                                     int64_t M, int64_t K, void* res_out, void* y, void* q,
+                                     void* s, bool ue8m0, cudaStream_t stream);
+
+// The router's choice of top_k of E experts per token and their weights.
+cudaError_t launch_moe_route(const void* logits, bool bf16, const float* bias, bool sigmoid,
+                             int64_t M, int64_t E, int64_t top_k, int64_t n_group,
+                             int64_t topk_group, bool renorm, float scale, int32_t* ids,
+                             float* weights, cudaStream_t stream);
+
+// The expert MLP of up to kMoeMaxM tokens (moe_mlp.cu).
+constexpr int64_t kMoeMaxM = 128;
+constexpr int64_t kMoeMaxE = 1024;
+constexpr int64_t kMoeMaxTopK = 32;
+struct MoeArgs {
+  const uint8_t* qa;        // [M][K]
+  const void* sa;           // [M][K/128] fp32 or UE8M0 codes
+  const int32_t* ids;       // [M][top_k]
+  const float* weights;     // [M][top_k]
+  const uint8_t* qg;        // [E][2I][K]
+  const void* sg;           // [E][2I/128][K/128]
+  const uint8_t* qd;        // [E][K][I]
+  const void* sd;           // [E][K/128][I/128]
+  __nv_bfloat16* y;         // [M][K]
+  int M, K, I, E, top_k;
+  int first_expert;
+  void* workspace;
+  long long wait_limit;
+  int* err;
+};
+size_t moe_workspace_bytes(int64_t M, int64_t K, int64_t I, int64_t E, int64_t top_k);
+int launch_moe_mlp(const MoeArgs& a, bool ue8m0, cudaStream_t stream);
 
 // Device address of the error word on the current device (cached per device).
 int* device_error_word();

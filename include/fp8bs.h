@@ -291,6 +291,110 @@ int fp8_gemm_swiglu_quant_noalloc(const void* qa, const float* sa, const void* q
 int fp8_gather_columns(const void* src_bf16, int64_t P, int64_t M, int64_t Np, void* dst_bf16,
                        void* stream);
 
+/*
+ * The input of a layer's FP8 linears from the residual stream: residual
+ * addition, root-mean-square norm and dynamic 1x128 quantization in one pass.
+ *
+ *   r = bf16_rn(x + residual)   (r = x when residual_bf16 is NULL)
+ *   n = r * w / sqrt(mean_k r^2 + eps)   in fp32, the mean over a row
+ *   y = bf16_rn(n),  s[m][g] = amax_{k in group g} |n| / 448,  q = e4m3(n / s)
+ *
+ *   x_bf16 [M][K]; residual_bf16 [M][K] or NULL; weight_bf16 [K] or NULL (ones).
+ *   residual_out_bf16 [M][K] or NULL: r. It may be the same pointer as
+ *       residual_bf16 or x_bf16 (an update in place); no other two buffers may
+ *       overlap.
+ *   y_bf16 [M][K] or NULL (the router of a mixture of experts reads it).
+ *   q_e4m3 [M][K], s [M][K/128] fp32 (the _ue8m0 form: codes, one byte each).
+ *   eps >= 0 and finite.
+ * The codes come from the fp32 n (not from y). They are those of e4m3(n / s)
+ * except where n / s lies within an fp32 ulp of the middle between two codes.
+ * K a positive multiple of 128, at most 65536. A row with a NaN, or an infinity,
+ * gives NaN in the groups where n is NaN.
+ */
+int fp8_add_rmsnorm_quant(const void* x_bf16, const void* residual_bf16, const void* weight_bf16,
+                          float eps, int64_t M, int64_t K, void* residual_out_bf16, void* y_bf16,
+                          void* q_e4m3, float* s, void* stream);
+int fp8_add_rmsnorm_quant_ue8m0(const void* x_bf16, const void* residual_bf16,
+                                const void* weight_bf16, float eps, int64_t M, int64_t K,
+                                void* residual_out_bf16, void* y_bf16, void* q_e4m3,
+                                uint8_t* s_ue8m0, void* stream);
+
+/*
+ * The router's choice for a mixture-of-experts layer: the top_k of E experts of
+ * every token from its logits, and their weights.
+ *
+ *   logits [M][E], fp32 (logits_bf16 == 0) or bf16 (!= 0).
+ *   bias [E] fp32 or NULL: added to the scores for the choice only, not in the
+ *       weights.
+ *   scoring: FP8BS_ROUTE_SOFTMAX or FP8BS_ROUTE_SIGMOID.
+ *   n_group, topk_group: with n_group > 1 the experts form n_group groups of
+ *       E / n_group neighbours; a group scores the sum of its two largest keys
+ *       (of its one, where only one is left) and only the experts of the
+ *       topk_group best groups can be chosen. n_group == 1: no groups.
+ *       A bias or groups need sigmoid scoring.
+ *   ids [M][top_k] int32, weights [M][top_k] fp32, output, by key, largest first.
+ *
+ * The key of an expert is its logit; with a bias or with groups it is
+ * sigmoid(logit) + bias, evaluated in double precision. Equal keys, and equal
+ * group scores, go to the lower index. An expert whose logit or bias is -inf or
+ * NaN is never chosen; a token left with fewer than top_k experts gets ids of -1
+ * with weight 0 in the last places. weights[m][j] is the softmax (over all
+ * experts whose logit is not -inf or NaN) or the sigmoid of the chosen logit;
+ * with renormalize != 0 divided by their sum + 1e-20; times `scale`.
+ *
+ *   1 <= E <= 1024; 1 <= top_k <= min(E, 32); 1 <= n_group <= 32 divides E;
+ *   1 <= topk_group <= n_group; top_k <= topk_group * (E / n_group). bf16 logits
+ *   need 2-byte alignment, all other pointers 4.
+ */
+#define FP8BS_ROUTE_SOFTMAX 0
+#define FP8BS_ROUTE_SIGMOID 1
+int moe_route_topk(const void* logits, int logits_bf16, const float* bias, int scoring, int64_t M,
+                   int64_t E, int64_t top_k, int64_t n_group, int64_t topk_group, int renormalize,
+                   float scale, int32_t* ids, float* weights, void* stream);
+
+/*
+ * The whole expert MLP of a mixture-of-experts layer for a few tokens (decode):
+ * gate+up, SwiGLU, quantization, down, and the weighted sum over a token's
+ * experts. For more tokens group the rows by expert and use fp8_grouped_gemm.
+ *
+ *   for token m and choice j with expert e = ids[m][j] - first_expert:
+ *     g, u = the block-scaled products (as fp8_block_gemm, in fp32) of qa[m]
+ *            with rows [0, I) and [I, 2I) of qw_gate_up[e]
+ *     h    = silu(g) * u in fp32; qh, sh = its 1x128 codes and scales along I
+ *     d_j  = the block-scaled product of qh with qw_down[e], in fp32
+ *   y[m] = bf16_rn(sum_j weights[m][j] * d_j)
+ *
+ *   qa [M][K], sa [M][K/128]; ids [M][top_k] int32, weights [M][top_k] fp32
+ *       (from moe_route_topk). A choice whose e is outside [0, E) adds nothing
+ *       (an id of -1; an expert of another rank: the weights here are those of
+ *       experts [first_expert, first_expert + E)); a token without a choice here
+ *       gets zeros. A token may name an expert more than once: the weights add.
+ *   qw_gate_up [E][2I][K], sw_gate_up [E][2I/128][K/128] ([W_gate; W_up]);
+ *   qw_down [E][K][I], sw_down [E][K/128][I/128].
+ *   y_bf16 [M][K], output.
+ *   workspace: at least fp8bs_moe_workspace_bytes(M, K, I, E, top_k) bytes, 16-byte
+ *       aligned; its contents need no preparation and mean nothing afterwards.
+ *       Calls that can run at the same time need workspaces of their own.
+ *   0 <= M <= 128, 1 <= E <= 1024, 1 <= top_k <= 32, first_expert >= 0; K and I
+ *   positive multiples of 128.
+ * The _ue8m0 form takes all scales as UE8M0 codes and quantizes h with them.
+ * Results are deterministic: the same inputs give the same bytes every call.
+ */
+int fp8_moe_mlp(const void* qa, const float* sa, const int32_t* ids, const float* weights,
+                const void* qw_gate_up, const float* sw_gate_up, const void* qw_down,
+                const float* sw_down, void* y_bf16, int64_t M, int64_t K, int64_t I, int64_t E,
+                int64_t top_k, int64_t first_expert, void* workspace, size_t workspace_bytes,
+                void* stream);
+int fp8_moe_mlp_ue8m0(const void* qa, const uint8_t* sa_ue8m0, const int32_t* ids,
+                      const float* weights, const void* qw_gate_up,
+                      const uint8_t* sw_gate_up_ue8m0, const void* qw_down,
+                      const uint8_t* sw_down_ue8m0, void* y_bf16, int64_t M, int64_t K, int64_t I,
+                      int64_t E, int64_t top_k, int64_t first_expert, void* workspace,
+                      size_t workspace_bytes, void* stream);
+
+/* Scratch bytes fp8_moe_mlp and fp8_moe_mlp_ue8m0 need (0 for an invalid shape). */
+size_t fp8bs_moe_workspace_bytes(int64_t M, int64_t K, int64_t I, int64_t E, int64_t top_k);
+
 /* Scratch bytes needed by the GEMMs for this shape (sparse != 0: the 2:4 GEMM). */
 size_t fp8bs_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K, int sparse);
 
