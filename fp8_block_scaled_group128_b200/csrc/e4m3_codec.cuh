@@ -268,18 +268,6 @@ __device__ __forceinline__ uint2 encode8f(const float (&x)[8], const ScaleDivide
   return make_uint2(codes4f(x[0], x[1], x[2], x[3], d), codes4f(x[4], x[5], x[6], x[7], d));
 }
 
-// One code (see codes4f).
-__device__ __forceinline__ uint32_t code1f(float x, const ScaleDivider& d) {
-  float q;
-  if (d.fast_all) {
-    const float q0 = __fmul_rn(x, d.r);
-    q = __fmaf_rn(__fmaf_rn(-q0, d.s, x), d.r, q0);
-  } else {
-    q = d.s == 0.0f ? x : d(x);
-  }
-  return __nv_cvt_float_to_fp8(q, __NV_SATFINITE, __NV_E4M3);
-}
-
 // The same against a power-of-two scale (the product is exact unless it
 // underflows).
 __device__ __forceinline__ uint32_t codes4f_pow2(float x0, float x1, float x2, float x3,

@@ -11,35 +11,53 @@
 // Bound: HBM. Every chosen expert's 3 I K weight bytes are read once, whatever
 // the number of its tokens; at the copy bandwidth an SM gets a 128 x 128 tile
 // (16 KB) every ~700 cycles, and both the MMAs and the promotion of a tile
-// take less than that for up to 128 tokens.
+// take less than that.
 //
-// Three launches, chained by programmatic dependent launch:
+// Two launches, chained by programmatic dependent launch:
 //
-//   moe_plan_kernel     one block: the chosen experts in order, each with its
-//                       list of tokens ("rows"), and the join counters zeroed
-//   moe_gemm_kernel<gate+up>  h's codes and scales, per row
-//   moe_gemm_kernel<down>     y
+//   moe_plan_kernel  one block: the chosen experts in order, each with its
+//                    tokens ("rows"), how the work is cut, the counters zeroed
+//   moe_mlp_kernel   one CTA per SM: gate+up and down
 //
-// Both GEMMs put 128 weight rows on the MMA's M side and an expert's tokens on
-// its N side (16 to 128, the expert's own count rounded up to 16). Their work
-// is a list of units, one 128-deep K-block of a tile each (gate and up of 128
-// intermediate columns; 128 output columns of one expert), in an order that
-// puts the units of a result next to each other. The list is cut into equal
-// contiguous ranges, one per CTA, so that every SM reads the same number of
-// weight bytes however many experts were chosen; a result whose units fall
-// into several CTAs is joined by the last of them to finish, which adds the
-// fp32 partial results in the order of the CTAs (the same bytes every call; no
-// CTA waits for another).
+// Both products put 128 weight rows on the MMA's M side and tokens on its N
+// side: the rows of one expert, in blocks of at most 64 (an expert with more is
+// walked twice; its weights then come from L2 the second time). The work is a
+// list of chunks: some K-blocks of one result (gate+up: expert and 128
+// intermediate columns; down: expert and 128 output columns). A CTA claims the
+// next chunk from a counter, streams its weights, writes the chunk's fp32
+// partial sums to the workspace and goes on; nothing in that stream waits for
+// another CTA. (Joining the parts inside the stream cost 4 us each time, most
+// of it the round trips of a fence and an atomic behind the weights in flight.)
 //
-//   warp 0        TMA producer: weight tiles and the tokens' K-block
-//   warp 1        MMA issuer: 4 (x 2) tcgen05.mma of K = 32 per unit into one
-//                 of the TMEM buffers
-//   warp 2        scale products sA * sW of 8 units at a time, into shared
-//                 memory
-//   warps 4..11   two promotion warpgroups, each half of the token columns:
-//                 TMEM -> registers times the scale products; at the end of a
-//                 tile SwiGLU and quantization, or the weighted sum over the
-//                 experts in shared memory
+// Finisher warps, of all CTAs, claim the results in the same order, wait for
+// their chunks and add the parts up in a fixed order, so that the bytes are
+// the same every call:
+//
+//   h   four rows x 128 intermediate columns: SwiGLU, codes and scales
+//   y   32 output columns of some tokens: the weighted sum over a token's experts
+//
+// Down's chunks follow gate+up's in the list, K-blocks first, then output
+// columns. A down chunk waits until h of its K-blocks is complete. All that a
+// chunk or a finisher waits for was claimed before, by CTAs that are running
+// and that in turn wait for earlier claims only, so every wait ends however few
+// of the CTAs are resident.
+//
+//   warp 0        claims chunks; TMA producer of the weight tiles
+//   warp 1        MMA issuer: 8 tcgen05.mma of K = 32 per unit (two tiles) into
+//                 one of the TMEM buffers
+//   warps 2, 4    scale products sA * sW of up to 8 units at a time, in turn,
+//                 into shared memory
+//   warp 3        TMA producer of the tokens' K-blocks
+//   warp 5        counts the chunks whose partial sums are written
+//   warps 6 ..    finishers (kFin)
+//   the last      promotion warpgroups, each a share of the token columns:
+//                 TMEM -> registers times the scale products -> workspace;
+//                 finishers when the chunks are used up
+//
+// The weights of a call evict the kernel's code from L2, so that the first pass
+// through each piece of code waits for HBM (about 1 us for 32 instructions
+// while the weights stream): what runs before the first tile is kept short, a
+// chunk is decoded once and handed on, and both products share their loops.
 //
 // Every wait is bounded as in gemm_kernel.cuh.
 #include <mutex>
@@ -52,49 +70,220 @@ namespace fp8bs {
 
 namespace {
 
-constexpr int kMaxCtas = 160;      // grid bound behind the workspace size
 constexpr int kPlanThreads = 1024;
+constexpr int kBlockRows = 64;     // tokens of one expert that are walked together
 constexpr int kBatch = 8;          // units per batch of scale products
-constexpr int kThreads = 384;
-constexpr int kPromo = 256;        // promotion threads
+constexpr int kTabs = 4;           // buffers of scale products
+constexpr int kFinRows = 4;        // rows of an h task
+constexpr int64_t kPartFloats = 8 << 20;   // partial sums of a product, but for large problems
 
-// What the plan kernel leaves for the GEMMs.
+constexpr int kSmemBytes = 227 * 1024;
+constexpr int kTileBytes = 128 * 128;
+constexpr int kUnitBytes = 2 * kTileBytes;
+constexpr int kMaxStages = 5;      // units in flight, at most
+constexpr int kMaxBufs = 16;       // TMEM buffers, at most
+constexpr int kMail = 8;           // chunks between claim and count, at most
+
+// How the work of a call is cut. A unit is 256 weight rows x 128 (gate+up: 128
+// gate rows and the 128 up rows of the same intermediate columns) or 128 x 256
+// (down: two K-blocks of 128 output columns; one at the end of an odd number).
+struct alignas(16) Head {
+  int blocks, rows;     // expert blocks; rows of all
+  int ncol, xbytes;     // TMEM columns of a product; bytes of a K-block of tokens
+  int stages, bufs;     // units in shared memory; TMEM buffers
+  int q_gu, cpt;        // units of a gate+up chunk; chunks of a result
+  int q_down, cps;      // units of a down chunk; chunks of a block's part of a result
+  int n_gu, total;      // chunks of gate+up; of both
+  int groups;           // h tasks of a gate+up result
+  int n_h, n_tasks;     // h tasks; of both kinds
+  int pad;
+};
+
+// What is known before the plan.
+struct Shape {
+  int M, K, I, top_k;
+  int sms;
+  int room;             // shared memory for units
+  int cap_gu, cap_down; // rows of partial sums that the workspace holds
+  int y_items;          // (token, 32 columns) of a y task
+  int y_tasks;          // y tasks of 128 output columns
+};
+
+// A chunk is about a twelfth of an SM's share, so that the SMs finish together
+// (they do not get equal bandwidth), but not below 8 units (one token through 2
+// experts of 4096 x 14336: 76 us with 4, 70 with 8, 72 with 16), nor below an
+// eighth of its tokens, where the partial sums weigh more than a quarter of the
+// weights. With less than 4 units for an SM, all SMs get some.
+__host__ __device__ inline int chunks_of(int units, int depth, int sms, int most, int cap) {
+  const int each = (units + sms - 1) / sms;
+  int q = each < 4 ? each : each < 96 ? 8 : each / 12;
+  const int least = most < 8 ? 1 : (most + 7) / 8;
+  if (q < least) q = least;
+  int n = (depth + q / 2) / q;
+  if (n > cap) n = cap;
+  return n < 1 ? 1 : n;
+}
+
+__host__ __device__ inline Head cut_work(int blocks, int rows, int most, const Shape& s) {
+  const int KB = s.K / 128, IB = s.I / 128, DU = (IB + 1) / 2;
+  Head h;
+  h.blocks = blocks;
+  h.rows = rows;
+  h.ncol = most <= 16 ? 16 : most <= 32 ? 32 : 64;
+  h.xbytes = (most + 15) / 16 * 2048;
+  h.stages = s.room / (kUnitBytes + 2 * h.xbytes);
+  if (h.stages > kMaxStages) h.stages = kMaxStages;
+  h.bufs = 256 / h.ncol;
+  const int r = rows < 1 ? 1 : rows;
+  h.cpt = chunks_of(blocks * IB * KB, KB, s.sms, most, s.cap_gu / r);
+  h.q_gu = (KB + h.cpt - 1) / h.cpt;
+  h.cpt = (KB + h.q_gu - 1) / h.q_gu;
+  h.cps = chunks_of(blocks * KB * DU, DU, s.sms, most, s.cap_down / r);
+  h.q_down = (DU + h.cps - 1) / h.cps;
+  h.cps = (DU + h.q_down - 1) / h.q_down;
+  h.n_gu = blocks * IB * h.cpt;
+  h.total = h.n_gu + blocks * h.cps * KB;
+  h.groups = (most + kFinRows - 1) / kFinRows;
+  h.n_h = blocks * IB * h.groups;
+  h.n_tasks = h.n_h + KB * s.y_tasks;
+  h.pad = 0;
+  return h;
+}
+
+// A chunk, as the producer of the weights hands it on.
+struct alignas(16) Chunk {
+  int kind;        // 0: gate+up, 1: down, -1: the end
+  int expert;
+  int row0, n;     // rows of the block
+  int tile;        // 128 intermediate, or output, columns
+  int c;           // chunk of the result (gate+up), of the block's part of it (down)
+  int k0, k1;      // units
+  int count;       // its counter
+  int ready;       // down: counter of the h tasks that it needs ...
+  int needs;       // ... and their number
+  int pad;
+};
+
+__host__ __device__ inline Chunk chunk_at(const Head& h, int t, int KB, int IB) {
+  Chunk ch;
+  int a, q, depth;
+  if (t >= h.n_gu) {
+    t -= h.n_gu;
+    const int s = t / KB;
+    ch.kind = 1;
+    ch.tile = t - s * KB;
+    a = s / h.cps;
+    ch.c = s - a * h.cps;
+    q = h.q_down;
+    depth = (IB + 1) / 2;
+    ch.count = ch.tile;
+  } else {
+    const int s = t / h.cpt;
+    ch.kind = 0;
+    ch.c = t - s * h.cpt;
+    a = s / IB;
+    ch.tile = s - a * IB;
+    q = h.q_gu;
+    depth = KB;
+    ch.count = s;
+  }
+  ch.expert = a;   // the block; its expert and rows are looked up
+  ch.row0 = ch.n = 0;
+  ch.k0 = ch.c * q;
+  ch.k1 = ch.k0 + q < depth ? ch.k0 + q : depth;
+  ch.ready = a * h.cps + ch.c;
+  ch.needs = ((2 * ch.k1 < IB ? 2 * ch.k1 : IB) - 2 * ch.k0) * h.groups;
+  ch.pad = 0;
+  return ch;
+}
+
+struct Barriers {
+  uint64_t fullw[kMaxStages], fullx[kMaxStages], empty[kMaxStages];
+  uint64_t tfull[kMaxBufs], tempty[kMaxBufs];
+  uint64_t sfull[kTabs], sempty[kTabs];
+  uint64_t mfull[kMail], mempty[kMail], dumped[kMail];
+  uint64_t mma_done, pairs;
+  static constexpr int kCount = 3 * kMaxStages + 2 * kMaxBufs + 2 * kTabs + 3 * kMail + 2;
+};
+
+struct alignas(16) Shared {
+  Chunk mail[kMail];
+  Barriers bar;
+  uint32_t tmem_slot;
+  int abort_flag;
+};
+
+// Shared memory of a CTA: Shared, the rows and weights of the choices [pairs],
+// the scale products, the units' weight tiles, their token blocks.
+struct Layout {
+  int off_row, off_w, off_tab, off_tiles;
+  __host__ Layout(int pairs, int ncol_max) {
+    off_row = static_cast<int>(sizeof(Shared));
+    off_w = off_row + (pairs * 2 + 15) / 16 * 16;
+    off_tab = off_w + (pairs * 4 + 15) / 16 * 16;
+    off_tiles = (off_tab + kTabs * kBatch * (2 * ncol_max + 4) * 4 + 1023) / 1024 * 1024;
+  }
+  __host__ int room() const { return kSmemBytes - 1024 - off_tiles; }
+};
+
+// What the plan kernel leaves for the MLP kernel.
 struct Plan {
-  int* n_act;        // number of chosen experts
-  int2* act;         // [n_act + 1]: (expert, its first row); the last entry ends the rows
+  Head* head;
+  int* ticket;       // [4]: chunks claimed; tasks claimed; h tasks complete; -
+  int2* act;         // [blocks + 1]: (expert, its first row); the last entry ends the rows
   int* row_tok;      // [rows] token of a row
-  float* row_w;      // [rows] weight of the row's token for its expert
-  int* count_gu;     // [n_act * I / 128] join counters of the gate+up tiles
-  int* count_down;   // [K / 128] join counters of the down tiles
+  int* pair_row;     // [M][top_k] row of a choice, or -1
+  float* pair_w;     // [M][top_k] its weight
+  int* counters;     // zeroed:
+  int* count_gu;     //   [blocks * I / 128] chunks written of a gate+up result
+  int* count_down;   //   [K / 128] chunks written of a down result
+  int* ready;        //   [blocks * units of I] h tasks complete of a down K-range
+  int n_counters;
 };
 
 struct Workspace {
   Plan plan;
-  uint8_t* qh;       // [rows][I]
-  void* sh;          // [rows][I / 128]
-  float* partial;    // [2 kMaxCtas][M][256] (gate+up) or [2 kMaxCtas][M][128] (down)
+  uint8_t* qh;         // [rows][I]
+  void* sh;            // [rows][I / 128]
+  float* part_gu;      // [chunks of a result][rows][I / 128][256]
+  float* part_down;    // [chunks of a block's part of a result][rows][K]
+  int cap_gu, cap_down;   // rows that they hold
   size_t bytes;
 };
 
 Workspace carve(void* base, int64_t M, int64_t K, int64_t I, int64_t E, int64_t top_k) {
-  const size_t rows = static_cast<size_t>(M * top_k);
-  const size_t act = static_cast<size_t>(E < M * top_k ? E : M * top_k);
+  const int64_t rows = M * top_k;
+  const int64_t act = (E < rows ? E : rows) + rows / (kBlockRows + 1);
   size_t at = 0;
   auto take = [&](size_t bytes) {
     uint8_t* p = static_cast<uint8_t*>(base) + at;
     at += (bytes + 255) / 256 * 256;
     return p;
   };
+  // as many parts as kPartFloats hold, from 1 to 64 where all choices are here
+  auto part_rows = [&](int64_t width) {
+    const int64_t parts = kPartFloats / (rows * width);
+    return static_cast<int>(rows * (parts < 1 ? 1 : parts > 64 ? 64 : parts));
+  };
   Workspace w;
-  w.plan.n_act = reinterpret_cast<int*>(take(4));
+  w.plan.head = reinterpret_cast<Head*>(take(sizeof(Head)));
+  w.plan.ticket = reinterpret_cast<int*>(take(16));
   w.plan.act = reinterpret_cast<int2*>(take((act + 1) * 8));
   w.plan.row_tok = reinterpret_cast<int*>(take(rows * 4));
-  w.plan.row_w = reinterpret_cast<float*>(take(rows * 4));
-  w.plan.count_gu = reinterpret_cast<int*>(take(act * (I / 128) * 4));
-  w.plan.count_down = reinterpret_cast<int*>(take(K / 128 * 4));
+  w.plan.pair_row = reinterpret_cast<int*>(take(rows * 4));
+  w.plan.pair_w = reinterpret_cast<float*>(take(rows * 4));
+  const int64_t n_gu = act * (I / 128), n_down = K / 128, n_ready = act * ((I / 128 + 1) / 2);
+  w.plan.counters = reinterpret_cast<int*>(take((n_gu + n_down + n_ready) * 4));
+  w.plan.count_gu = w.plan.counters;
+  w.plan.count_down = w.plan.count_gu + n_gu;
+  w.plan.ready = w.plan.count_down + n_down;
+  w.plan.n_counters = static_cast<int>(n_gu + n_down + n_ready);
   w.qh = take(rows * I);
   w.sh = take(rows * (I / 128) * 4);
-  w.partial = reinterpret_cast<float*>(take(static_cast<size_t>(2 * kMaxCtas) * M * 256 * 4));
+  w.cap_gu = part_rows(2 * I);
+  w.cap_down = part_rows(K);
+  w.part_gu = reinterpret_cast<float*>(take(static_cast<size_t>(w.cap_gu) * 2 * I * 4));
+  w.part_down = reinterpret_cast<float*>(take(static_cast<size_t>(w.cap_down) * K * 4));
   w.bytes = at;
   return w;
 }
@@ -103,23 +292,32 @@ Workspace carve(void* base, int64_t M, int64_t K, int64_t I, int64_t E, int64_t 
 // A choice counts once per token and expert: of a token's choices of the same
 // expert the first one makes the row and carries the sum of their weights (in
 // the order of the choices). The order of an expert's rows comes from atomics
-// and may differ from call to call; nothing computed depends on it.
+// and may differ from call to call; nothing computed depends on it. The block
+// has a thread for every expert at least, and two warps at least.
 __global__ void __launch_bounds__(kPlanThreads)
     moe_plan_kernel(const int32_t* __restrict__ ids, const float* __restrict__ weights, int pairs,
-                    int top_k, int E, int first_expert, int n_gu, int n_down, Plan plan) {
+                    int E, int first_expert, const Plan plan, const Shape shape) {
   __shared__ int expert[kMoeMaxM * kMoeMaxTopK];   // local expert of a choice, -1: none
-  __shared__ int fill[kMoeMaxE];                   // next row of an expert
+  __shared__ float share[kMoeMaxM * kMoeMaxTopK];  // weight of a choice
+  __shared__ int fill[kPlanThreads];               // next row of an expert
   __shared__ uint32_t warp_sum[kPlanThreads / 32];
-  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  __shared__ int most;
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5, T = blockDim.x;
+  const int top_k = shape.top_k;
   fill[t] = 0;
+  if (t < kPlanThreads / 32) warp_sum[t] = 0u;
+  if (t == 0) most = 0;
   grid_dependency_wait();
   grid_launch_dependents();
-  for (int i = t; i < pairs; i += kPlanThreads) {
+#pragma unroll 1
+  for (int i = t; i < pairs; i += T) {
     const int64_t e = static_cast<int64_t>(ids[i]) - first_expert;
+    share[i] = weights[i];
     expert[i] = e >= 0 && e < E ? static_cast<int>(e) : -1;
   }
-  for (int i = t; i < n_gu; i += kPlanThreads) plan.count_gu[i] = 0;
-  for (int i = t; i < n_down; i += kPlanThreads) plan.count_down[i] = 0;
+#pragma unroll 1
+  for (int i = t; i < plan.n_counters; i += T) plan.counters[i] = 0;
+  if (t < 4) plan.ticket[t] = 0;
   __syncthreads();
   auto is_row = [&](int i) {   // the token's first choice of this expert
     if (expert[i] < 0) return false;
@@ -127,12 +325,15 @@ __global__ void __launch_bounds__(kPlanThreads)
       if (expert[j] == expert[i]) return false;
     return true;
   };
-  for (int i = t; i < pairs; i += kPlanThreads)
+#pragma unroll 1
+  for (int i = t; i < pairs; i += T)
     if (is_row(i)) atomicAdd(&fill[expert[i]], 1);
   __syncthreads();
-  // exclusive prefix over the experts of (chosen experts << 16 | rows): at
-  // most 1024 experts and 4096 rows
-  const uint32_t mine = fill[t] > 0 ? (1u << 16) | static_cast<uint32_t>(fill[t]) : 0u;
+  // exclusive prefix over the experts of (blocks << 16 | rows): at most 4096
+  // rows, in at most 1024 + 63 blocks
+  const int n = fill[t];
+  const int blocks = (n + kBlockRows - 1) / kBlockRows;
+  const uint32_t mine = (static_cast<uint32_t>(blocks) << 16) | static_cast<uint32_t>(n);
   uint32_t scan = mine;
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
@@ -140,634 +341,760 @@ __global__ void __launch_bounds__(kPlanThreads)
     if (lane >= off) scan += o;
   }
   if (lane == 31) warp_sum[warp] = scan;
+  // rows of the largest block (a block count of 1 or 2)
+  const int top = __reduce_max_sync(0xffffffffu, blocks > 1 ? (n + 1) / 2 : n);
+  if (lane == 0 && top > 0) atomicMax(&most, top);
   __syncthreads();
-  uint32_t before = 0u, total = 0u;
-  {
-    const uint32_t s = warp_sum[lane];
-    total = __reduce_add_sync(0xffffffffu, s);
-    before = __reduce_add_sync(0xffffffffu, lane < warp ? s : 0u);
-  }
+  const uint32_t sums = warp_sum[lane];
+  const uint32_t total = __reduce_add_sync(0xffffffffu, sums);
+  const uint32_t before = __reduce_add_sync(0xffffffffu, lane < warp ? sums : 0u);
   const uint32_t excl = before + scan - mine;
-  if (mine != 0u) plan.act[excl >> 16] = make_int2(t, static_cast<int>(excl & 0xFFFFu));
-  fill[t] = static_cast<int>(excl & 0xFFFFu);
-  if (t == 0) {
-    *plan.n_act = static_cast<int>(total >> 16);
-    plan.act[total >> 16] = make_int2(-1, static_cast<int>(total & 0xFFFFu));
-  }
+  const int row0 = static_cast<int>(excl & 0xFFFFu);
+  if (blocks > 0) plan.act[excl >> 16] = make_int2(t, row0);
+  if (blocks > 1) plan.act[(excl >> 16) + 1] = make_int2(t, row0 + n / 2);
+  fill[t] = row0;
   __syncthreads();
-  for (int i = t; i < pairs; i += kPlanThreads) {
-    if (!is_row(i)) continue;
-    const int end = i / top_k * top_k + top_k;
-    float w = weights[i];
-    for (int j = i + 1; j < end; ++j)
-      if (expert[j] == expert[i]) w += weights[j];
-    const int row = atomicAdd(&fill[expert[i]], 1);
-    plan.row_tok[row] = i / top_k;
-    plan.row_w[row] = w;
+  if (t == T - 1) {
+    const int rows = static_cast<int>(total & 0xFFFFu);
+    plan.act[total >> 16] = make_int2(-1, rows);
+    *plan.head = cut_work(static_cast<int>(total >> 16), rows, most, shape);
+  }
+#pragma unroll 1
+  for (int i = t; i < pairs; i += T) {
+    int row = -1;
+    float w = share[i];
+    if (is_row(i)) {
+      const int end = i / top_k * top_k + top_k;
+      for (int j = i + 1; j < end; ++j)
+        if (expert[j] == expert[i]) w += share[j];
+      row = atomicAdd(&fill[expert[i]], 1);
+      plan.row_tok[row] = i / top_k;
+    }
+    plan.pair_row[i] = row;
+    plan.pair_w[i] = w;
   }
 }
 
-// ------------------------------------------------------------------- GEMMs --
-struct GemmMoeArgs {
+// --------------------------------------------------------------------- MLP --
+struct MlpArgs {
   Plan plan;
-  const void* sx;    // scales of the token operand: sa [M][K/128], or sh [rows][I/128]
-  const void* sw;    // weight scales: [E][2I/128][K/128], or [E][K/128][I/128]
-  uint8_t* qh;       // gate+up: the codes of h [rows][I]
-  void* sh;          // gate+up: their scales [rows][I/128]
-  __nv_bfloat16* y;  // down: [M][K]
-  float* partial;
-  int M, K, I;
+  Shape shape;
+  const void* sa;    // [M][K/128]
+  const void* sg;    // [E][2I/128][K/128]
+  const void* sd;    // [E][K/128][I/128]
+  uint8_t* qh;       // [rows][I]
+  void* sh;          // [rows][I/128]
+  __nv_bfloat16* y;  // [M][K]
+  float* part_gu;
+  float* part_down;
+  int off_row, off_w, off_tab, off_tiles;
   long long wait_limit;
   int* err;
 };
 
 __device__ __forceinline__ float scale_value(const void* s, int64_t i, bool e8) {
-  if (!e8) return static_cast<const float*>(s)[i];
-  const uint32_t c = static_cast<const uint8_t*>(s)[i];
+  if (!e8) return __ldcg(static_cast<const float*>(s) + i);
+  const uint32_t c = __ldcg(static_cast<const uint8_t*>(s) + i);
   return c == 0u ? __uint_as_float(0x00400000u) : __uint_as_float(c << 23);
 }
 
-template <int kN, bool kDown>
-struct MoeCfg {
-  static_assert(kN == 16 || kN == 32 || kN == 64 || kN == 128, "token columns");
-  static constexpr int kParts = kDown ? 1 : 2;             // weight tiles per unit
-  static constexpr int kWBytes = kParts * 128 * 128;
-  static constexpr int kXBytes = kN * 128;
-  static constexpr int kStageBytes = kWBytes + kXBytes;
-  static constexpr int kBufCols = kParts * kN;             // TMEM columns of a unit
-  static constexpr int kBufs = 512 / kBufCols < 8 ? 512 / kBufCols : 8;
-  static constexpr int kTmemCols =
-      kBufs * kBufCols <= 128 ? 128 : kBufs * kBufCols <= 256 ? 256 : 512;
-  // scale products: [2 batches][kBatch][kParts][kN], a unit's row padded
-  static constexpr int kRow = kParts * kN + 4;
-  static constexpr int kTabBytes = 2 * kBatch * kRow * 4;
-  // end of a tile: gate+up: codes [kN][128] and warp maxima [kN][4];
-  // down: the fp32 sums [kN tokens][128]
-  static constexpr int kEndBytes = kDown ? kN * 128 * 4 : kN * 128 + kN * 16;
-  static constexpr int kActBytes = (static_cast<int>(kMoeMaxE) + 1) * 8;
-  static constexpr int kFixed = kTabBytes + kEndBytes + kActBytes + 1024 /* barriers */ + 1024;
-  static constexpr int kFit = (227 * 1024 - kFixed) / kStageBytes;
-  static constexpr int kStages = kFit < 12 ? kFit : 12;
-  static_assert(kStages >= 3, "at least three stages");
-  static constexpr int kOffX = kStages * kWBytes;
-  static constexpr int kOffTab = kOffX + kStages * kXBytes;
-  static constexpr int kOffEnd = kOffTab + kTabBytes;
-  static constexpr int kOffAct = kOffEnd + kEndBytes;
-  static constexpr int kOffBar = kOffAct + (kActBytes + 15) / 16 * 16;
-  static constexpr int kNumBars = 2 * kStages + 2 * kBufs + 4 + 1;
-  static constexpr int kOffMisc = kOffBar + kNumBars * 8;
-  static constexpr int kSmemBytes = kOffMisc + 16 + 1024;
-  static_assert(kSmemBytes <= 227 * 1024, "shared memory");
-  static constexpr int kHalf = kN / 2;                     // columns of a promotion thread, at most
+__device__ __forceinline__ int load_acquire(const int* p) {
+  int v;
+  asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+
+// Orders this thread's generic-proxy accesses before later async-proxy (TMA)
+// accesses, in global memory too.
+__device__ __forceinline__ void fence_proxy_async_all() {
+  asm volatile("fence.proxy.async;" ::: "memory");
+}
+
+__device__ __forceinline__ int load_relaxed(const int* p) {
+  int v;
+  asm volatile("ld.relaxed.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+
+// Waits until *p >= target, for at most `limit` cycles; the whole warp. (Only
+// the last load acquires: an acquire empties the SM's L1.)
+__device__ __forceinline__ bool wait_count_warp(const int* p, int target, long long limit) {
+  const long long t0 = clock64();
+  bool ok = true;
+  while (load_relaxed(p) < target) {
+    if (clock64() - t0 > limit) {
+      ok = false;
+      break;
+    }
+    __nanosleep(100);
+  }
+  return __all_sync(0xffffffffu, ok && load_acquire(p) >= target);
+}
+
+// *p >= target now; the whole warp.
+__device__ __forceinline__ bool wait_now_warp(const int* p, int target) {
+  return __all_sync(0xffffffffu, load_relaxed(p) >= target) &&
+         __all_sync(0xffffffffu, load_acquire(p) >= target);
+}
+
+__device__ __forceinline__ void add4(float4& a, const float4& b) {
+  a.x += b.x;
+  a.y += b.y;
+  a.z += b.z;
+  a.w += b.w;
+}
+
+__device__ __forceinline__ float4 shfl_xor4(const float4& a, int off) {
+  return make_float4(__shfl_xor_sync(0xffffffffu, a.x, off), __shfl_xor_sync(0xffffffffu, a.y, off),
+                     __shfl_xor_sync(0xffffffffu, a.z, off), __shfl_xor_sync(0xffffffffu, a.w, off));
+}
+
+struct Ring {   // position in a ring of n barriers
+  int i = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void next(int n) {
+    if (++i == n) {
+      i = 0;
+      phase ^= 1u;
+    }
+  }
 };
 
-// The unit list of one launch and this CTA's range of it. A tile is one result
-// (gate+up: expert and group of 128 intermediate columns; down: 128 output
-// columns, over all experts); a segment is the part of it that is walked with
-// one set of token rows.
-struct Range {
-  int64_t begin, end, units;
-  int ctas;   // CTAs that have work: each has at least one unit
-  __device__ __forceinline__ Range(int64_t u, int grid, int cta) : units(u) {
-    ctas = u < grid ? static_cast<int>(u) : grid;
-    begin = cta < ctas ? u * cta / ctas : u;
-    end = cta < ctas ? u * (cta + 1) / ctas : u;
-  }
-  __device__ __forceinline__ int owner(int64_t unit) const {
-    return static_cast<int>(((unit + 1) * ctas - 1) / units);
-  }
-  __device__ __forceinline__ int64_t begin_of(int cta) const { return units * cta / ctas; }
-};
-
-template <int kN, bool kDown, bool kE8>
-__global__ void __launch_bounds__(kThreads, 1)
-    moe_gemm_kernel(const __grid_constant__ CUtensorMap tmap_w,
-                    const __grid_constant__ CUtensorMap tmap_x, const GemmMoeArgs args) {
-  using C = MoeCfg<kN, kDown>;
+// kN: most token columns; kWgs: promotion warpgroups; kFin: finisher warps (2
+// modulo 4, so that the promotion warps begin at a multiple of 4).
+template <int kN, int kWgs, int kFin, bool kE8>
+__global__ void __launch_bounds__(32 * (6 + kFin) + 128 * kWgs, 1)
+    moe_mlp_kernel(const __grid_constant__ CUtensorMap tmap_g,
+                   const __grid_constant__ CUtensorMap tmap_d,
+                   const __grid_constant__ CUtensorMap tmap_a,
+                   const __grid_constant__ CUtensorMap tmap_h,
+                   const __grid_constant__ MlpArgs args) {
+  constexpr int kPromo0 = 6 + kFin;    // first promotion warp
+  constexpr int kPer = kN / kWgs;      // columns of a promotion thread, at most
+  static_assert(kPer % 8 == 0, "promotion works on eight columns at a time");
+  static_assert(kPromo0 % 4 == 0, "a promotion warp's TMEM lanes go by its number");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  uint8_t* sm_w = smem;
-  uint8_t* sm_x = smem + C::kOffX;
-  float* tab = reinterpret_cast<float*>(smem + C::kOffTab);
-  int2* act = reinterpret_cast<int2*>(smem + C::kOffAct);
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
-  uint64_t* empty = full + C::kStages;
-  uint64_t* tfull = empty + C::kStages;
-  uint64_t* tempty = tfull + C::kBufs;
-  uint64_t* sfull = tempty + C::kBufs;
-  uint64_t* sempty = sfull + 2;
-  uint64_t* mma_done = sempty + 2;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
-  volatile int* last_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 8);
+  Shared& sh = *reinterpret_cast<Shared*>(smem);
+  Barriers& bar = sh.bar;
+  volatile int* abort_flag = &sh.abort_flag;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const long long limit = args.wait_limit;
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < C::kStages; ++i) {
-      mbar_init(&full[i], 1);
-      mbar_init(&empty[i], 1);
-    }
-    for (int i = 0; i < C::kBufs; ++i) {
-      mbar_init(&tfull[i], 1);
-      mbar_init(&tempty[i], kPromo / 32);
-    }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&sfull[i], 1);
-      mbar_init(&sempty[i], kPromo / 32);
-    }
-    mbar_init(mma_done, 1);
-    *abort_flag = 0;
+  if (threadIdx.x < Barriers::kCount) {
+    // arrivals: one, but for those of the promotion warps, of a chunk's readers
+    // (its place in the ring: warps 1 to 5 and promotion) and of the finishers
+    uint64_t* b = reinterpret_cast<uint64_t*>(&bar) + threadIdx.x;
+    uint32_t count = 1;
+    if ((b >= bar.tempty && b < bar.tempty + kMaxBufs) ||
+        (b >= bar.sempty && b < bar.sempty + kTabs) || (b >= bar.dumped && b < bar.dumped + kMail))
+      count = 4 * kWgs;
+    if (b >= bar.mempty && b < bar.mempty + kMail) count = 5 + 4 * kWgs;
+    if (b == &bar.pairs) count = kFin;
+    mbar_init(b, count);
     fence_mbarrier_init();
-    tma_prefetch_desc(&tmap_w);
-    tma_prefetch_desc(&tmap_x);
+  }
+  if (threadIdx.x == 0) {
+    sh.abort_flag = 0;
+    tma_prefetch_desc(&tmap_g);
+    tma_prefetch_desc(&tmap_d);
+    tma_prefetch_desc(&tmap_a);
+    tma_prefetch_desc(&tmap_h);
   }
   if (warp == 1) {
-    tmem_alloc(tmem_slot, C::kTmemCols);
+    tmem_alloc(&sh.tmem_slot, 512);
     tmem_relinquish();
   }
-  grid_dependency_wait();
-  grid_launch_dependents();
-  const int n_act = __ldcg(args.plan.n_act);
-  for (int i = threadIdx.x; i <= n_act; i += kThreads) act[i] = __ldcg(args.plan.act + i);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem_base = *tmem_slot;
-
-  const int IB = args.I / 128, KB = args.K / 128;
-  const int depth = kDown ? IB : KB;                   // units of a segment
-  const int tile_units = kDown ? n_act * IB : KB;      // units of a tile
-  const Range range(static_cast<int64_t>(kDown ? KB : IB) * n_act * depth,
-                    static_cast<int>(gridDim.x), static_cast<int>(blockIdx.x));
-  // segment s: expert index and tile coordinate
-  auto seg_act = [&](int64_t s) { return static_cast<int>(kDown ? s % n_act : s / IB); };
-  auto seg_tile = [&](int64_t s) { return static_cast<int>(kDown ? s / n_act : s % IB); };
+  const uint32_t tmem_base = sh.tmem_slot;
+  grid_dependency_wait();
+  grid_launch_dependents();
+  int ticket = 0;
+  if (threadIdx.x == 0) ticket = atomicAdd(args.plan.ticket, 1);
+  Head head;
+#pragma unroll
+  for (int i = 0; i < static_cast<int>(sizeof(Head)) / 16; ++i)
+    reinterpret_cast<int4*>(&head)[i] = __ldcg(reinterpret_cast<const int4*>(args.plan.head) + i);
+  const int KB = args.shape.K / 128, IB = args.shape.I / 128;
+  float* tab = reinterpret_cast<float*>(smem + args.off_tab);
+  uint8_t* tiles = smem + args.off_tiles;
+  uint8_t* xtiles = tiles + head.stages * kUnitBytes;
+  const int tab_row = 2 * head.ncol + 4;   // floats of a unit's scale products, padded
+  const int2* act = args.plan.act;
+  const int* row_tok = args.plan.row_tok;
+  int* h_done = args.plan.ticket + 2;
 
   auto stopped = [&]() { return __any_sync(0xffffffffu, *abort_flag != 0) != 0; };
+  auto give_up = [&]() {
+    if (lane == 0) record_device_error(args.err, FP8BS_ERR_DEVICE_TIMEOUT);
+    *abort_flag = 1;
+  };
+  // The next chunk for a reader of the ring; false at the end. `keep` leaves
+  // its place in the ring occupied.
+  Ring mr;
+  auto next_chunk = [&](Chunk& ch, bool keep) {
+    bool ok = !stopped();
+    if (ok) {
+      ok = mbar_wait_warp(&bar.mfull[mr.i], mr.phase, limit);
+      if (!ok) give_up();
+    }
+    if (!ok) return false;
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+      reinterpret_cast<int4*>(&ch)[i] = reinterpret_cast<const int4*>(&sh.mail[mr.i])[i];
+    if (ch.kind < 0) return false;
+    __syncwarp();
+    if (!keep) {
+      if (lane == 0) mbar_arrive(&bar.mempty[mr.i]);
+      mr.next(kMail);
+    }
+    return true;
+  };
+  // h of a down chunk's K-blocks is complete
+  bool all_ready = false;
+  auto wait_h = [&](const Chunk& ch) {
+    if (all_ready) return true;
+    all_ready = wait_now_warp(h_done, head.n_h);
+    return all_ready || wait_count_warp(args.plan.ready + ch.ready, ch.needs, limit);
+  };
 
   if (warp == 0) {
-    // -------------------------------------------------------- TMA producer --
-    int stage = 0;
-    uint32_t phase = 0;
+    // -------------------------------------------- chunks and weight tiles --
+    Ring r;
     int issued = 0;
-    for (int64_t u = range.begin; u < range.end && !stopped();) {
-      const int64_t s = u / depth;
-      const int k0 = static_cast<int>(u - s * depth);
-      const int k1 = static_cast<int>(min(static_cast<int64_t>(depth), k0 + range.end - u));
-      const int a = seg_act(s), tile = seg_tile(s);
-      const int e = act[a].x, row0 = act[a].y, n = act[a + 1].y - row0;
-      const int wrow = kDown ? e * args.K + tile * 128 : e * 2 * args.I + tile * 128;
-      int tok[4] = {0, 0, 0, 0};
-      const int n4 = (n + 3) / 4, n16 = (n + 15) / 16;
-      if (!kDown && lane < n4) {
-#pragma unroll
-        for (int q = 0; q < 4; ++q) tok[q] = args.plan.row_tok[row0 + min(4 * lane + q, n - 1)];
+    bool ok = true;
+    // read once: the partial sums and the kernel's code should stay in L2
+    // instead (231 -> 223 us for 64 tokens on 32 experts of 7168 x 2048)
+    const uint64_t policy = policy_evict_first();
+    ticket = __shfl_sync(0xffffffffu, ticket, 0);
+    while (!stopped()) {
+      const bool end = ticket >= head.total;
+      Chunk ch = chunk_at(head, ticket, KB, IB);
+      if (end) {
+        ch.kind = -1;
+      } else {
+        const int2 b = act[ch.expert];
+        const int2 b1 = act[ch.expert + 1];
+        ch.n = b1.y - b.y;
+        ch.expert = b.x;
+        ch.row0 = b.y;
       }
-      const uint32_t bytes = C::kWBytes + (kDown ? n16 * 2048 : n4 * 512);
-      for (int k = k0; k < k1; ++k) {
-        if (!mbar_wait_warp(&empty[stage], phase ^ 1u, limit)) {
-          if (lane == 0) record_device_error(args.err, FP8BS_ERR_DEVICE_TIMEOUT);
-          *abort_flag = 1;
-          break;
-        }
-        uint8_t* w = sm_w + stage * C::kWBytes;
-        uint8_t* x = sm_x + stage * C::kXBytes;
+      ok = mbar_wait_warp(&bar.mempty[mr.i], mr.phase ^ 1u, limit);
+      if (!ok) break;
+      int next = 0;
+      if (lane == 0) {
+        sh.mail[mr.i] = ch;
+        mbar_arrive(&bar.mfull[mr.i]);
+        // the answer comes while this chunk's loads are issued
+        if (!end) next = atomicAdd(args.plan.ticket, 1);
+      }
+      __syncwarp();
+      mr.next(kMail);
+      if (end) break;
+      // a unit's tiles: gate+up (k, y) and (k, y + I); down (2k, y) and (2k + 1, y)
+      const bool down = ch.kind != 0;
+      const CUtensorMap* map = down ? &tmap_d : &tmap_g;
+      const int y = ch.expert * (down ? args.shape.K : 2 * args.shape.I) + ch.tile * 128;
+      const int y2 = down ? y : y + args.shape.I;
+      const int step = down ? 256 : 128, dx = down ? 128 : 0;
+#pragma unroll 1
+      for (int k = ch.k0; k < ch.k1; ++k) {
+        ok = mbar_wait_warp(&bar.empty[r.i], r.phase ^ 1u, limit);
+        if (!ok) break;
+        const bool two = !down || 2 * k + 1 < IB;
         if (elect_one()) {
-          mbar_arrive_expect_tx(&full[stage], bytes);
-          tma_load_2d(w, &tmap_w, &full[stage], k * 128, wrow);
-          if constexpr (!kDown) tma_load_2d(w + 16384, &tmap_w, &full[stage], k * 128, wrow + args.I);
-          if constexpr (kDown) {
-            for (int i = 0; i < n16; ++i)
-              tma_load_2d(x + i * 2048, &tmap_x, &full[stage], k * 128, row0 + i * 16);
-          }
+          uint8_t* to = tiles + r.i * kUnitBytes;
+          mbar_arrive_expect_tx(&bar.fullw[r.i], two ? kUnitBytes : kTileBytes);
+          tma_load_2d_hint(to, map, &bar.fullw[r.i], k * step, y, policy);
+          if (two)
+            tma_load_2d_hint(to + kTileBytes, map, &bar.fullw[r.i], k * step + dx, y2, policy);
         }
         __syncwarp();
-        if (!kDown && lane < n4)
-          tma_gather4_2d(x + lane * 512, &tmap_x, &full[stage], k * 128, tok[0], tok[1], tok[2],
-                         tok[3]);
         ++issued;
-        if (++stage == C::kStages) {
-          stage = 0;
-          phase ^= 1u;
-        }
+        r.next(head.stages);
       }
-      u += k1 - k0;
+      if (!ok) break;
+      ticket = __shfl_sync(0xffffffffu, next, 0);
     }
+    if (!ok) give_up();
     // every copy issued must have landed before the CTA exits
-    const int pending = issued < C::kStages ? issued : C::kStages;
+    const int pending = issued < head.stages ? issued : head.stages;
+#pragma unroll 1
     for (int i = 0; i < pending; ++i) {
-      int st = stage - 1 - i;
-      uint32_t ph = phase;
+      int st = r.i - 1 - i;
+      uint32_t ph = r.phase;
       if (st < 0) {
-        st += C::kStages;
+        st += head.stages;
         ph ^= 1u;
       }
-      mbar_wait(&full[st], ph, kDefaultWaitCycles);
+      mbar_wait(&bar.fullw[st], ph, kDefaultWaitCycles);
     }
   } else if (warp == 1) {
     // ---------------------------------------------------------- MMA issuer --
-    int stage = 0, tb = 0;
-    uint32_t phase = 0, tphase = 0;
+    Ring r, b;
     bool ok = true;
-    const uint64_t dw0 = sw128_kmajor_desc(smem_u32(sm_w));
-    const uint64_t dx0 = sw128_kmajor_desc(smem_u32(sm_x));
-    for (int64_t u = range.begin; ok && u < range.end && !stopped();) {
-      const int64_t s = u / depth;
-      const int k0 = static_cast<int>(u - s * depth);
-      const int k1 = static_cast<int>(min(static_cast<int64_t>(depth), k0 + range.end - u));
-      const int a = seg_act(s);
-      const int n = act[a + 1].y - act[a].y;
-      const uint32_t idesc = idesc_e4m3_f32(128, (n + 15) / 16 * 16);
-      for (int k = k0; ok && k < k1; ++k) {
-        if (!mbar_wait_warp(&full[stage], phase, limit) ||
-            !mbar_wait_warp(&tempty[tb], tphase ^ 1u, limit)) {
-          ok = false;
-          break;
-        }
+    const uint64_t dw0 = sw128_kmajor_desc(smem_u32(tiles));
+    const uint64_t dx0 = sw128_kmajor_desc(smem_u32(xtiles));
+    Chunk ch;
+    while (ok && next_chunk(ch, false)) {
+      const uint32_t idesc = idesc_e4m3_f32(128, (ch.n + 15) / 16 * 16);
+#pragma unroll 1
+      for (int k = ch.k0; k < ch.k1; ++k) {
+        ok = mbar_wait_warp(&bar.tempty[b.i], b.phase ^ 1u, limit) &&
+             mbar_wait_warp(&bar.fullx[r.i], r.phase, limit) &&
+             mbar_wait_warp(&bar.fullw[r.i], r.phase, limit);
+        if (!ok) break;
         tc_fence_after();
-        const uint64_t dw = dw0 + static_cast<uint32_t>((stage * C::kWBytes) >> 4);
-        const uint64_t dx = dx0 + static_cast<uint32_t>((stage * C::kXBytes) >> 4);
-        const uint32_t d = tmem_base + static_cast<uint32_t>(tb * C::kBufCols);
+        const uint64_t dw = dw0 + static_cast<uint32_t>((r.i * kUnitBytes) >> 4);
+        const uint64_t dx = dx0 + static_cast<uint32_t>((r.i * 2 * head.xbytes) >> 4);
+        const uint32_t d = tmem_base + static_cast<uint32_t>(b.i * 2 * head.ncol);
+        // the second product: of gate+up's other tile with the same tokens, of
+        // down's next K-block; the first again (times 0 later) where that is missing
+        const bool two = ch.kind == 0 || 2 * k + 1 < IB;
+        const uint64_t ew = dw + (two ? kTileBytes >> 4 : 0);
+        const uint64_t ex = dx + static_cast<uint32_t>(two && ch.kind != 0 ? head.xbytes >> 4 : 0);
+        const uint32_t e = d + static_cast<uint32_t>(head.ncol);
         if (elect_one()) {
-#pragma unroll
-          for (int p = 0; p < C::kParts; ++p) {
-            const uint64_t dp = dw + static_cast<uint32_t>((p * 16384) >> 4);
-            const uint32_t dd = d + static_cast<uint32_t>(p * kN);
-            mma_f8f6f4_c<false>(dd, dp, dx, idesc);
-            mma_f8f6f4_c<true>(dd, dp + (32 >> 4), dx + (32 >> 4), idesc);
-            mma_f8f6f4_c<true>(dd, dp + (64 >> 4), dx + (64 >> 4), idesc);
-            mma_f8f6f4_c<true>(dd, dp + (96 >> 4), dx + (96 >> 4), idesc);
-          }
-          mma_commit(&tfull[tb]);
-          mma_commit(&empty[stage]);
+          mma_f8f6f4_c<false>(d, dw, dx, idesc);
+          mma_f8f6f4_c<true>(d, dw + (32 >> 4), dx + (32 >> 4), idesc);
+          mma_f8f6f4_c<true>(d, dw + (64 >> 4), dx + (64 >> 4), idesc);
+          mma_f8f6f4_c<true>(d, dw + (96 >> 4), dx + (96 >> 4), idesc);
+          mma_f8f6f4_c<false>(e, ew, ex, idesc);
+          mma_f8f6f4_c<true>(e, ew + (32 >> 4), ex + (32 >> 4), idesc);
+          mma_f8f6f4_c<true>(e, ew + (64 >> 4), ex + (64 >> 4), idesc);
+          mma_f8f6f4_c<true>(e, ew + (96 >> 4), ex + (96 >> 4), idesc);
+          mma_commit(&bar.tfull[b.i]);
+          mma_commit(&bar.empty[r.i]);
         }
         __syncwarp();
-        if (++tb == C::kBufs) {
-          tb = 0;
-          tphase ^= 1u;
-        }
-        if (++stage == C::kStages) {
-          stage = 0;
-          phase ^= 1u;
-        }
+        r.next(head.stages);
+        b.next(head.bufs);
       }
-      u += k1 - k0;
     }
-    if (!ok) {
-      if (lane == 0) record_device_error(args.err, FP8BS_ERR_DEVICE_TIMEOUT);
-      *abort_flag = 1;
-    }
-    if (elect_one()) mma_commit(mma_done);
+    if (!ok) give_up();
+    if (elect_one()) mma_commit(&bar.mma_done);
     __syncwarp();
-    mbar_wait(mma_done, 0, kDefaultWaitCycles);
-  } else if (warp == 2) {
+    mbar_wait(&bar.mma_done, 0, kDefaultWaitCycles);
+  } else if (warp == 2 || warp == 4) {
     // -------------------------------------------------------- scale products --
-    // A batch is up to 8 consecutive units of a segment; lane: unit j = lane % 8
-    // and columns lane / 8, + 4, + 8, ... (a column's 8 scales lie next to each
-    // other in memory).
+    // A batch is up to 8 consecutive units of a chunk; the two warps take them
+    // in turn. Lane: unit j = lane % 8 and columns lane / 8, + 4, + 8, ... (a
+    // column's 8 scales lie next to each other in memory). The loads of a batch
+    // (of its first columns) are under way before the buffer is waited for.
     const int j = lane & 7;
-    int buf = 0;
-    uint32_t phase = 0;
+    constexpr int kLoads = 4;
+    Ring b;
     bool ok = true;
-    for (int64_t u = range.begin; ok && u < range.end && !stopped();) {
-      const int64_t s = u / depth;
-      const int k0 = static_cast<int>(u - s * depth);
-      const int k1 = static_cast<int>(min(static_cast<int64_t>(depth), k0 + range.end - u));
-      const int a = seg_act(s), tile = seg_tile(s);
-      const int e = act[a].x, row0 = act[a].y, n = act[a + 1].y - row0;
-      const int64_t w0 = kDown ? (static_cast<int64_t>(e) * KB + tile) * IB
-                               : (static_cast<int64_t>(e) * 2 * IB + tile) * KB;
-      const int64_t w1 = w0 + static_cast<int64_t>(IB) * KB;   // the up block's scales
-      for (int k = k0; ok && k < k1; k += kBatch) {
-        const bool on = k + j < k1;
-        float sw0 = 0.0f, sw1 = 0.0f;
-        if (on) {
-          sw0 = scale_value(args.sw, w0 + k + j, kE8);
-          if constexpr (!kDown) sw1 = scale_value(args.sw, w1 + k + j, kE8);
+    Chunk ch;
+    while (ok && next_chunk(ch, false)) {
+      const bool down = ch.kind != 0;
+      const void* sw = down ? args.sd : args.sg;
+      const void* sx = down ? args.sh : args.sa;
+      const int kbs = down ? IB : KB;   // scales of a row
+      const int64_t w0 =
+          (static_cast<int64_t>(ch.expert) * (down ? KB : 2 * IB) + ch.tile) * kbs;
+      const int64_t w1 = down ? 1 : static_cast<int64_t>(IB) * kbs;   // to the second tile's
+      const int x1 = down ? 1 : 0;
+      bool waited = !down;
+#pragma unroll 1
+      for (int k = ch.k0; k < ch.k1; k += kBatch, b.next(kTabs)) {
+        if ((b.i & 1) != (warp == 4)) continue;
+        const int kb = down ? 2 * (k + j) : k + j;       // the unit's (first) K-block
+        const bool on = k + j < ch.k1;
+        const bool two = on && (!down || kb + 1 < kbs);
+        const float s0 = on ? scale_value(sw, w0 + kb, kE8) : 0.0f;
+        const float s1 = two ? scale_value(sw, w0 + kb + w1, kE8) : 0.0f;
+        if (!waited) {
+          ok = wait_h(ch);
+          if (!ok) break;
+          waited = true;
         }
-        if (!mbar_wait_warp(&sempty[buf], phase ^ 1u, limit)) {
-          ok = false;
-          break;
-        }
-        float* out = tab + (buf * kBatch + j) * C::kRow;
-        for (int c = lane >> 3; c < n; c += 16) {
-          float v[4];
+        float* out = tab + (b.i * kBatch + j) * tab_row;
+#pragma unroll 1
+        for (int c0 = 0; c0 < ch.n; c0 += 4 * kLoads) {
+          float v[kLoads], z[kLoads];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int cc = c + 4 * i;
-            v[i] = 0.0f;
-            if (on && cc < n) {
-              const int row = kDown ? row0 + cc : args.plan.row_tok[row0 + cc];
-              v[i] = scale_value(args.sx, static_cast<int64_t>(row) * depth + k + j, kE8);
+          for (int i = 0; i < kLoads; ++i) {
+            const int c = c0 + (lane >> 3) + 4 * i;
+            v[i] = z[i] = 0.0f;
+            if (c < ch.n && on) {
+              const int64_t at =
+                  static_cast<int64_t>(down ? ch.row0 + c : row_tok[ch.row0 + c]) * kbs + kb;
+              v[i] = scale_value(sx, at, kE8);
+              if (two) z[i] = scale_value(sx, at + x1, kE8);
             }
           }
+          if (c0 == 0) {
+            ok = mbar_wait_warp(&bar.sempty[b.i], b.phase ^ 1u, limit);
+            if (!ok) break;
+          }
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            if (c + 4 * i < n) {
-              out[c + 4 * i] = v[i] * sw0;
-              if constexpr (!kDown) out[kN + c + 4 * i] = v[i] * sw1;
+          for (int i = 0; i < kLoads; ++i) {
+            const int c = c0 + (lane >> 3) + 4 * i;
+            if (c < ch.n) {
+              out[c] = v[i] * s0;
+              out[head.ncol + c] = z[i] * s1;
             }
           }
+        }
+        if (!ok) break;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.sfull[b.i]);
+      }
+    }
+    if (!ok) give_up();
+  } else if (warp == 3) {
+    // -------------------------------------------------------- token blocks --
+    Ring r;
+    int issued = 0;
+    bool ok = true;
+    Chunk ch;
+    while (ok && next_chunk(ch, false)) {
+      const bool down = ch.kind != 0;
+      const int n4 = (ch.n + 3) / 4, n16 = (ch.n + 15) / 16;
+      int tok[4] = {0, 0, 0, 0};
+      if (down) {
+        const bool fenced = all_ready;
+        ok = wait_h(ch);
+        if (!fenced) fence_proxy_async_all();   // h's codes were written through the generic proxy
+      } else if (lane < n4) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) tok[q] = row_tok[ch.row0 + min(4 * lane + q, ch.n - 1)];
+      }
+#pragma unroll 1
+      for (int k = ch.k0; ok && k < ch.k1; ++k) {
+        ok = mbar_wait_warp(&bar.empty[r.i], r.phase ^ 1u, limit);
+        if (!ok) break;
+        uint8_t* to = xtiles + r.i * 2 * head.xbytes;
+        const bool two = down && 2 * k + 1 < IB;
+        if (elect_one())
+          mbar_arrive_expect_tx(&bar.fullx[r.i], down ? n16 * (two ? 4096 : 2048) : n4 * 512);
+        __syncwarp();
+        if (!down) {
+          if (lane < n4)
+            tma_gather4_2d(to + lane * 512, &tmap_a, &bar.fullx[r.i], k * 128, tok[0], tok[1],
+                           tok[2], tok[3]);
+        } else if (lane < 2 * n16 && (two || !(lane & 1))) {
+          tma_load_2d(to + (lane & 1) * head.xbytes + (lane >> 1) * 2048, &tmap_h,
+                      &bar.fullx[r.i], k * 256 + (lane & 1) * 128, ch.row0 + (lane >> 1) * 16);
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sfull[buf]);
-        if (++buf == 2) {
-          buf = 0;
-          phase ^= 1u;
-        }
+        ++issued;
+        r.next(head.stages);
       }
-      u += k1 - k0;
     }
-    if (!ok) {
-      if (lane == 0) record_device_error(args.err, FP8BS_ERR_DEVICE_TIMEOUT);
-      *abort_flag = 1;
+    if (!ok) give_up();
+    const int pending = issued < head.stages ? issued : head.stages;
+#pragma unroll 1
+    for (int i = 0; i < pending; ++i) {
+      int st = r.i - 1 - i;
+      uint32_t ph = r.phase;
+      if (st < 0) {
+        st += head.stages;
+        ph ^= 1u;
+      }
+      mbar_wait(&bar.fullx[st], ph, kDefaultWaitCycles);
     }
-  } else if (warp >= 4) {
+  } else if (warp == 5) {
+    // ------------------------------------------------------ counts chunks --
+    // A chunk's place in the ring is given back only here and after its count,
+    // which keeps `dumped` within one phase.
+    Chunk ch;
+    bool ok = true;
+    while (ok && next_chunk(ch, true)) {
+      ok = mbar_wait_warp(&bar.dumped[mr.i], mr.phase, limit);
+      if (ok && lane == 0) {
+        __threadfence();   // the partial sums of all promotion warps before the count
+        atomicAdd((ch.kind != 0 ? args.plan.count_down : args.plan.count_gu) + ch.count, 1);
+        mbar_arrive(&bar.mempty[mr.i]);
+      }
+      __syncwarp();
+      mr.next(kMail);
+    }
+    if (!ok) give_up();
+  } else if (warp >= kPromo0) {
     // ------------------------------------------------------------ promotion --
-    const int wg = (warp - 4) >> 2;
+    const int wg = (warp - kPromo0) >> 2;
     const int quarter = warp & 3;
     const int row = quarter * 32 + lane;                  // weight row of the tile
-    const int pt = static_cast<int>(threadIdx.x) - 128;   // 0 .. 255
     const uint32_t tlane = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16);
-    uint8_t* codes = smem + C::kOffEnd;                                  // gate+up: [kN][128]
-    uint32_t* maxima = reinterpret_cast<uint32_t*>(smem + C::kOffEnd + kN * 128);   // [kN][4]
-    float* sums = reinterpret_cast<float*>(smem + C::kOffEnd);           // down: [kN][128]
-    int tb = 0, buf = 0;
-    uint32_t tphase = 0, sphase = 0;
+    const int ncol = head.ncol;
+    Ring tb, sb;
     bool ok = true;
-    float acc[C::kParts][C::kHalf];
-
-    // Hands one result's partial values (already in this CTA's slot) to the
-    // other CTAs that have parts of it; true in the last one, which adds them.
-    auto join = [&](int* counter, int parts) {
-      __threadfence();
-      named_bar_sync(1, kPromo);
-      if (pt == 0) {
-        const int before = ok ? atomicAdd(counter, 1) : -1;
-        __threadfence();
-        *last_flag = before == parts - 1 ? 1 : 0;
+    Chunk ch;
+    for (;;) {
+      const int slot = mr.i;
+      if (!next_chunk(ch, false)) break;
+      // this warpgroup's columns: [col0, col0 + cols)
+      const int per = (ch.n + 8 * kWgs - 1) / (8 * kWgs) * 8;
+      const int col0 = wg * per;
+      const int cols = max(0, min(per, (ch.n + 7) / 8 * 8 - col0));
+      // the two products of the chunk's units times their scale products
+      float acc[2][kPer];
+#pragma unroll
+      for (int p = 0; p < 2; ++p)
+#pragma unroll
+        for (int c = 0; c < kPer; ++c) acc[p][c] = 0.0f;
+#pragma unroll 1
+      for (int k = ch.k0; k < ch.k1; ++k) {
+        const int j = (k - ch.k0) % kBatch;
+        const bool batch_end = j == kBatch - 1 || k == ch.k1 - 1;
+        if (j == 0) ok = mbar_wait_warp(&bar.sfull[sb.i], sb.phase, limit);
+        ok = ok && mbar_wait_warp(&bar.tfull[tb.i], tb.phase, limit);
+        if (!ok) break;
+        tc_fence_after();
+        const float* sc = tab + (sb.i * kBatch + j) * tab_row + col0;
+        const uint32_t ta = tlane + static_cast<uint32_t>(tb.i * 2 * ncol + col0);
+#pragma unroll
+        for (int c = 0; c < kPer; c += 8) {
+          if (c < cols) {
+            float v[2][8];
+#pragma unroll
+            for (int p = 0; p < 2; ++p) tmem_ld8(ta + p * ncol + c, v[p]);
+            tmem_wait_ld();
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+#pragma unroll
+              for (int i = 0; i < 8; i += 4) {
+                const float4 q = *reinterpret_cast<const float4*>(sc + p * ncol + c + i);
+                fma2(acc[p][c + i], acc[p][c + i + 1], v[p][i], v[p][i + 1], q.x, q.y);
+                fma2(acc[p][c + i + 2], acc[p][c + i + 3], v[p][i + 2], v[p][i + 3], q.z, q.w);
+              }
+            }
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&bar.tempty[tb.i]);
+          if (batch_end) mbar_arrive(&bar.sempty[sb.i]);
+        }
+        if (batch_end) sb.next(kTabs);
+        tb.next(head.bufs);
       }
-      named_bar_sync(1, kPromo);
-      __threadfence();
-      return *last_flag != 0;
-    };
-    // slot of a CTA's part of the tile that begins at unit t0: 0 if the CTA's
-    // range begins in the tile, else 1 (the tile is its last)
-    auto slot_of = [&](int cta, int64_t t0) {
-      return 2 * cta + (range.begin_of(cta) >= t0 ? 0 : 1);
-    };
-    if constexpr (kDown) {
-      for (int i = pt; i < args.M * 128; i += kPromo) sums[i] = 0.0f;
-      named_bar_sync(1, kPromo);
+      if (!ok) break;
+      // gate+up: both values; down: their sum
+      const bool down = ch.kind != 0;
+      const int64_t step = down ? args.shape.K : static_cast<int64_t>(IB) * 256;
+      float* to = (down ? args.part_down + ch.tile * 128 : args.part_gu + ch.tile * 256) +
+                  (static_cast<int64_t>(ch.c) * head.rows + ch.row0 + col0) * step + row;
+#pragma unroll
+      for (int c = 0; c < kPer; ++c) {
+        if (col0 + c < ch.n && c < cols) {
+          __stcg(to + c * step, down ? acc[0][c] + acc[1][c] : acc[0][c]);
+          if (!down) __stcg(to + c * step + 128, acc[1][c]);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar.dumped[slot]);
     }
-
-    for (int64_t u = range.begin; u < range.end;) {
-      const int64_t s = u / depth;
-      const int k0 = static_cast<int>(u - s * depth);
-      const int k1 = static_cast<int>(min(static_cast<int64_t>(depth), k0 + range.end - u));
-      const int a = seg_act(s), tile = seg_tile(s);
-      const int row0 = act[a].y, n = act[a + 1].y - row0;
-      const int half = (n + 15) / 16 * 8;     // columns of each warpgroup
-      const int col0 = wg * half;
-#pragma unroll
-      for (int p = 0; p < C::kParts; ++p)
-#pragma unroll
-        for (int c = 0; c < C::kHalf; ++c) acc[p][c] = 0.0f;
-
-      for (int k = k0; k < k1; ++k) {
-        const int j = (k - k0) % kBatch;
-        if (ok && j == 0) ok = mbar_wait(&sfull[buf], sphase, limit);
-        if (ok) ok = mbar_wait(&tfull[tb], tphase, limit);
-        ok = __all_sync(0xffffffffu, ok);
-        if (ok) {
-          tc_fence_after();
-          const float* sc = tab + (buf * kBatch + j) * C::kRow + col0;
-          const uint32_t ta = tlane + static_cast<uint32_t>(tb * C::kBufCols + col0);
-#pragma unroll
-          for (int c = 0; c < C::kHalf; c += 8) {
-            if (c < half) {
-              float v[C::kParts][8];
-#pragma unroll
-              for (int p = 0; p < C::kParts; ++p) tmem_ld8(ta + p * kN + c, v[p]);
-              tmem_wait_ld();
-#pragma unroll
-              for (int p = 0; p < C::kParts; ++p) {
-#pragma unroll
-                for (int i = 0; i < 8; i += 4) {
-                  const float4 q = *reinterpret_cast<const float4*>(sc + p * kN + c + i);
-                  fma2(acc[p][c + i], acc[p][c + i + 1], v[p][i], v[p][i + 1], q.x, q.y);
-                  fma2(acc[p][c + i + 2], acc[p][c + i + 3], v[p][i + 2], v[p][i + 3], q.z, q.w);
-                }
-              }
-            }
-          }
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&tempty[tb]);
-          if (lane == 0 && (j == kBatch - 1 || k == k1 - 1)) mbar_arrive(&sempty[buf]);
-        }
-        if (j == kBatch - 1 || k == k1 - 1) {
-          if (++buf == 2) {
-            buf = 0;
-            sphase ^= 1u;
-          }
-        }
-        if (++tb == C::kBufs) {
-          tb = 0;
-          tphase ^= 1u;
-        }
+    if (!ok) give_up();
+    tc_fence_before();
+  }
+  if (warp >= 6) {
+    // ------------------------------------------------------------ finishers --
+    bool ok = true;
+    int16_t* pair_row = reinterpret_cast<int16_t*>(smem + args.off_row);
+    float* pair_w = reinterpret_cast<float*>(smem + args.off_w);
+    if (warp < kPromo0) {   // for the promotion warps too: y is long after
+#pragma unroll 1
+      for (int i = threadIdx.x - 192; i < args.shape.M * args.shape.top_k; i += 32 * kFin) {
+        pair_row[i] = static_cast<int16_t>(__ldcg(args.plan.pair_row + i));
+        pair_w[i] = __ldcg(args.plan.pair_w + i);
       }
-      u += k1 - k0;
-
-      if constexpr (!kDown) {
-        const int64_t t0 = s * depth;
-        bool mine = true;
-        if (k1 - k0 < depth) {   // the tile's K range is shared with other CTAs
-          float* part = args.partial +
-                        static_cast<int64_t>(slot_of(blockIdx.x, t0)) * args.M * 256 + row;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar.pairs);
+    }
+    bool pairs_there = false;
+    const int64_t gu_row = static_cast<int64_t>(IB) * 256;   // floats of a row of part_gu
+    while (!stopped()) {
+      int task = 0;
+      if (lane == 0) task = atomicAdd(args.plan.ticket + 1, 1);
+      task = __shfl_sync(0xffffffffu, task, 0);
+      if (task >= head.n_tasks) break;
+      if (task < head.n_h) {
+        // h = silu(g) * u of up to 8 rows: the warp has a row's 128 columns, a
+        // lane four of them
+        const int s = task / head.groups;
+        const int a = s / IB, tile = s - a * IB;
+        const int row0 = act[a].y + (task - s * head.groups) * kFinRows;
+        const int row1 = min(row0 + kFinRows, act[a + 1].y);
+        if (row0 < row1) ok = wait_count_warp(args.plan.count_gu + s, head.cpt, limit);
+        if (!ok) break;
+#pragma unroll 1
+        for (int row = row0; row < row1; ++row) {
+          const float4* from =
+              reinterpret_cast<const float4*>(args.part_gu + row * gu_row + tile * 256) + lane;
+          const int64_t part = head.rows * gu_row / 4;
+          float4 g = make_float4(0.0f, 0.0f, 0.0f, 0.0f), u = g;
+#pragma unroll 1
+          for (int q = 0; q < head.cpt; q += 4) {
+            float4 x[4], z[4];
 #pragma unroll
-          for (int c = 0; c < C::kHalf; ++c) {
-            if (c < half && col0 + c < n) {
-              __stcg(part + (col0 + c) * 256, acc[0][c]);
-              __stcg(part + (col0 + c) * 256 + 128, acc[1][c]);
-            }
-          }
-          const int c0 = range.owner(t0), c1 = range.owner(t0 + depth - 1);
-          mine = join(args.plan.count_gu + s, c1 - c0 + 1);
-          if (mine) {
-#pragma unroll
-            for (int p = 0; p < C::kParts; ++p)
-#pragma unroll
-              for (int c = 0; c < C::kHalf; ++c) acc[p][c] = 0.0f;
-            for (int q = c0; q <= c1; ++q) {
-              const float* from =
-                  args.partial + static_cast<int64_t>(slot_of(q, t0)) * args.M * 256 + row;
-#pragma unroll
-              for (int c = 0; c < C::kHalf; ++c) {
-                if (c < half && col0 + c < n) {
-                  acc[0][c] += __ldcg(from + (col0 + c) * 256);
-                  acc[1][c] += __ldcg(from + (col0 + c) * 256 + 128);
-                }
+            for (int i = 0; i < 4; ++i) {
+              x[i] = z[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+              if (q + i < head.cpt) {
+                x[i] = __ldcg(from + (q + i) * part);
+                z[i] = __ldcg(from + (q + i) * part + 32);
               }
             }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              add4(g, x[i]);
+              add4(u, z[i]);
+            }
           }
+          const float h[4] = {silu_f32(g.x) * u.x, silu_f32(g.y) * u.y, silu_f32(g.z) * u.z,
+                              silu_f32(g.w) * u.w};
+          // magnitudes are compared as integers, so that a NaN is the largest
+          uint32_t m = 0u;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) m = max(m, __float_as_uint(h[i]) & 0x7FFFFFFFu);
+          const float amax = __uint_as_float(__reduce_max_sync(0xffffffffu, m));
+          const int64_t at = static_cast<int64_t>(row) * IB + tile;
+          uint32_t q;
+          if constexpr (kE8) {
+            const uint32_t code = ue8m0_code_of_amax(amax);
+            q = codes4f_pow2(h[0], h[1], h[2], h[3], ue8m0_inv_scale(code));
+            if (lane == 0) static_cast<uint8_t*>(args.sh)[at] = static_cast<uint8_t>(code);
+          } else {
+            const float sc = scale_of_amax(amax);
+            q = codes4f(h[0], h[1], h[2], h[3], ScaleDivider(sc));
+            if (lane == 0) static_cast<float*>(args.sh)[at] = sc;
+          }
+          *reinterpret_cast<uint32_t*>(args.qh + at * 128 + lane * 4) = q;
         }
-        if (mine) {   // the same in all promotion warps, unlike ok: barriers follow
-          // h = silu(g) * u of this thread's intermediate column; a token's
-          // group of 128 lies across the warpgroup's threads
-#pragma unroll
-          for (int c = 0; c < C::kHalf; ++c) {
-            if (c < half) {
-              acc[0][c] = silu_f32(acc[0][c]) * acc[1][c];
-              const uint32_t m =
-                  __reduce_max_sync(0xffffffffu, __float_as_uint(acc[0][c]) & 0x7FFFFFFFu);
-              if (lane == 0) maxima[(col0 + c) * 4 + quarter] = m;
-            }
-          }
-          named_bar_sync(2 + wg, 128);
-#pragma unroll
-          for (int c = 0; c < C::kHalf; ++c) {
-            if (c < half && col0 + c < n) {
-              const uint4 m4 = *reinterpret_cast<const uint4*>(maxima + (col0 + c) * 4);
-              const float amax = __uint_as_float(max(max(m4.x, m4.y), max(m4.z, m4.w)));
-              const int64_t at = static_cast<int64_t>(row0 + col0 + c) * IB + tile;
-              uint32_t q;
-              if constexpr (kE8) {
-                const uint32_t code = ue8m0_code_of_amax(amax);
-                q = __nv_cvt_float_to_fp8(acc[0][c] * ue8m0_inv_scale(code), __NV_SATFINITE,
-                                          __NV_E4M3);
-                if (row == 0) static_cast<uint8_t*>(args.sh)[at] = static_cast<uint8_t>(code);
-              } else {
-                const float sc = scale_of_amax(amax);
-                q = code1f(acc[0][c], ScaleDivider(sc));
-                if (row == 0) static_cast<float*>(args.sh)[at] = sc;
-              }
-              codes[(col0 + c) * 128 + row] = static_cast<uint8_t>(q);
-            }
-          }
-          named_bar_sync(2 + wg, 128);
-          for (int i = row; i < half * 8; i += 128) {   // 16-byte chunks
-            const int c = col0 + (i >> 3);
-            if (ok && c < n)
-              *reinterpret_cast<uint4*>(args.qh + static_cast<int64_t>(row0 + c) * args.I +
-                                        tile * 128 + (i & 7) * 16) =
-                  *reinterpret_cast<const uint4*>(codes + c * 128 + (i & 7) * 16);
-          }
+        fence_proxy_async_all();   // TMA reads the codes
+        __syncwarp();
+        if (lane == 0) {
+          __threadfence();
+          atomicAdd(args.plan.ready + a * head.cps + tile / 2 / head.q_down, 1);
+          atomicAdd(h_done, 1);
         }
       } else {
-        // this expert's share of the tokens' sums
-        const int* toks = args.plan.row_tok + row0;
-        const float* ws = args.plan.row_w + row0;
+        // y of some (token, quarter of the 128 columns). Eight lanes have an
+        // item's 32 columns; the warp's 16 slots (four groups of lanes, four
+        // registers) are the parts of one item or, where it has fewer, of several
+        const int s = task - head.n_h;
+        const int tile = s / args.shape.y_tasks;
+        const int item0 = (s - tile * args.shape.y_tasks) * args.shape.y_items;
+        const int item1 = min(item0 + args.shape.y_items, 4 * args.shape.M);
+        ok = wait_count_warp(args.plan.count_down + tile, head.blocks * head.cps, limit);
+        if (!ok) break;
+        if (!pairs_there) ok = mbar_wait_warp(&bar.pairs, 0, limit);
+        if (!ok) break;
+        pairs_there = true;
+        // part p: chunk p % cps of choice p / cps
+        const int parts = args.shape.top_k * head.cps;
+        const int lg = parts > 8 ? 4 : parts > 4 ? 3 : parts > 2 ? 2 : parts - 1;   // slots of an item
+        const int grp = lane >> 3;
+#pragma unroll 1
+        for (int it = item0; it < item1; it += 16 >> lg) {
+          float4 v[4];
 #pragma unroll
-        for (int c = 0; c < C::kHalf; ++c) {
-          if (c < half && col0 + c < n) {
-            float* at = sums + toks[col0 + c] * 128 + row;
-            *at = fmaf(ws[col0 + c], acc[0][c], *at);
-          }
-        }
-        const int64_t t0 = static_cast<int64_t>(tile) * tile_units;
-        // between two segments too: the next expert's columns may put a token
-        // into the other warpgroup
-        named_bar_sync(1, kPromo);
-        if (u == range.end || u == t0 + tile_units) {
-          // the end of this CTA's part of the tile; a warp takes every eighth
-          // token, a lane four of its 128 columns
-          const bool whole = range.begin <= t0 && u == t0 + tile_units;
-          const int pw = pt >> 5;
-          const int c0 = range.owner(t0), c1 = range.owner(t0 + tile_units - 1);
-          bool mine = true;
-          if (!whole) {
-            float4* part = reinterpret_cast<float4*>(
-                args.partial + static_cast<int64_t>(slot_of(blockIdx.x, t0)) * args.M * 128);
-            for (int m = pw; m < args.M; m += kPromo / 32)
-              __stcg(part + m * 32 + lane, reinterpret_cast<const float4*>(sums)[m * 32 + lane]);
-            mine = join(args.plan.count_down + tile, c1 - c0 + 1);
-          }
-          if (mine && ok) {
-            for (int m = pw; m < args.M; m += kPromo / 32) {
-              float4 v = reinterpret_cast<const float4*>(sums)[m * 32 + lane];
-              if (!whole) {
-                v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                for (int q = c0; q <= c1; ++q) {
-                  const float4 o = __ldcg(
-                      reinterpret_cast<const float4*>(
-                          args.partial + static_cast<int64_t>(slot_of(q, t0)) * args.M * 128) +
-                      m * 32 + lane);
-                  v.x += o.x;
-                  v.y += o.y;
-                  v.z += o.z;
-                  v.w += o.w;
+          for (int i = 0; i < 4; ++i) v[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 1
+          for (int p0 = 0; p0 < parts; p0 += 1 << lg) {
+            float4 x[4];
+            float w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int slot = 4 * i + grp;
+              const int item = it + (slot >> lg), p = p0 + (slot & ((1 << lg) - 1));
+              x[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+              w[i] = 0.0f;
+              if (item < item1 && p < parts) {
+                const int j = p / head.cps;
+                const int pair = (item >> 2) * args.shape.top_k + j;
+                const int r = pair_row[pair];
+                if (r >= 0) {
+                  w[i] = pair_w[pair];
+                  x[i] = __ldcg(reinterpret_cast<const float4*>(
+                                    args.part_down +
+                                    (static_cast<int64_t>(p - j * head.cps) * head.rows + r) *
+                                        args.shape.K +
+                                    tile * 128 + (item & 3) * 32) +
+                                (lane & 7));
                 }
               }
-              const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y);
-              const __nv_bfloat162 hi = __floats2bfloat162_rn(v.z, v.w);
-              *reinterpret_cast<uint2*>(args.y + static_cast<int64_t>(m) * args.K + tile * 128 +
-                                        lane * 4) =
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              v[i].x = fmaf(w[i], x[i].x, v[i].x);
+              v[i].y = fmaf(w[i], x[i].y, v[i].y);
+              v[i].z = fmaf(w[i], x[i].z, v[i].z);
+              v[i].w = fmaf(w[i], x[i].w, v[i].w);
+            }
+          }
+          // an item's slots: registers first, then groups of lanes
+          if (lg >= 3) {
+            add4(v[0], v[1]);
+            add4(v[2], v[3]);
+          }
+          if (lg == 4) add4(v[0], v[2]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int slot = 4 * i;
+            if ((slot & ((1 << lg) - 1)) != 0) continue;   // the same in all lanes
+            if (lg >= 1) add4(v[i], shfl_xor4(v[i], 8));
+            if (lg >= 2) add4(v[i], shfl_xor4(v[i], 16));
+            const int item = it + ((slot + grp) >> lg);
+            if (item < item1 && (grp & ((1 << lg) - 1)) == 0) {
+              const __nv_bfloat162 lo = __floats2bfloat162_rn(v[i].x, v[i].y);
+              const __nv_bfloat162 hi = __floats2bfloat162_rn(v[i].z, v[i].w);
+              *reinterpret_cast<uint2*>(args.y + static_cast<int64_t>(item >> 2) * args.shape.K +
+                                        tile * 128 + (item & 3) * 32 + (lane & 7) * 4) =
                   make_uint2(*reinterpret_cast<const uint32_t*>(&lo),
                              *reinterpret_cast<const uint32_t*>(&hi));
             }
           }
-          named_bar_sync(1, kPromo);
-          for (int i = pt; i < args.M * 128; i += kPromo) sums[i] = 0.0f;
-          named_bar_sync(1, kPromo);
         }
       }
     }
-    if (!ok) {
-      if (lane == 0) record_device_error(args.err, FP8BS_ERR_DEVICE_TIMEOUT);
-      *abort_flag = 1;
-    }
-    if constexpr (kDown) {
-      if (n_act == 0) {   // no token has a choice here
-        const int64_t total = static_cast<int64_t>(args.M) * args.K / 8;
-        for (int64_t i = static_cast<int64_t>(blockIdx.x) * kPromo + pt; i < total;
-             i += static_cast<int64_t>(gridDim.x) * kPromo)
-          reinterpret_cast<uint4*>(args.y)[i] = make_uint4(0u, 0u, 0u, 0u);
-      }
-    }
-    tc_fence_before();
+    if (!ok) give_up();
   }
   __syncthreads();
   if (warp == 1) {
     __syncwarp();
     tc_fence_after();
-    tmem_dealloc(tmem_base, C::kTmemCols);
+    tmem_dealloc(tmem_base, 512);
   }
 }
 
-template <int kN, bool kDown, bool kE8>
-int launch_gemm(const CUtensorMap& tw, const CUtensorMap& tx, const GemmMoeArgs& args, int grid,
-                int device, cudaStream_t stream) {
-  using C = MoeCfg<kN, kDown>;
-  auto kern = moe_gemm_kernel<kN, kDown, kE8>;
+template <int kN, int kWgs, int kFin, bool kE8>
+int launch_mlp(const CUtensorMap (&maps)[4], const MlpArgs& args, int grid, int device,
+               cudaStream_t stream) {
+  auto kern = moe_mlp_kernel<kN, kWgs, kFin, kE8>;
   static std::once_flag flags[64];
   cudaError_t attr_err = cudaSuccess;
   std::call_once(flags[device], [&] {
-    attr_err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+    attr_err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
   });
   if (attr_err != cudaSuccess) return FP8BS_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
-  cfg.blockDim = dim3(kThreads, 1, 1);
-  cfg.dynamicSmemBytes = C::kSmemBytes;
+  cfg.blockDim = dim3(32 * (6 + kFin) + 128 * kWgs, 1, 1);
+  cfg.dynamicSmemBytes = kSmemBytes;
   cfg.stream = stream;
   cudaLaunchAttribute pdl;
   pdl.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   pdl.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &pdl;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, tw, tx, args) == cudaSuccess ? FP8BS_OK : FP8BS_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, kern, maps[0], maps[1], maps[2], maps[3], args) == cudaSuccess
+             ? FP8BS_OK
+             : FP8BS_ERR_CUDA;
 }
 
-template <bool kDown, bool kE8>
-int launch_gemm_n(const CUtensorMap& tw, const CUtensorMap& tx, const GemmMoeArgs& args, int grid,
-                  int device, cudaStream_t stream) {
-  if (args.M <= 16) return launch_gemm<16, kDown, kE8>(tw, tx, args, grid, device, stream);
-  if (args.M <= 32) return launch_gemm<32, kDown, kE8>(tw, tx, args, grid, device, stream);
-  if (args.M <= 64) return launch_gemm<64, kDown, kE8>(tw, tx, args, grid, device, stream);
-  return launch_gemm<128, kDown, kE8>(tw, tx, args, grid, device, stream);
+template <bool kE8>
+int launch_mlp_n(const CUtensorMap (&maps)[4], const MlpArgs& args, int device,
+                 cudaStream_t stream) {
+  if (args.shape.M <= 16) return launch_mlp<16, 2, 2, kE8>(maps, args, args.shape.sms, device, stream);
+  if (args.shape.M <= 32) return launch_mlp<32, 2, 2, kE8>(maps, args, args.shape.sms, device, stream);
+  return launch_mlp<64, 2, 2, kE8>(maps, args, args.shape.sms, device, stream);
 }
 
 }  // namespace
@@ -779,54 +1106,64 @@ size_t moe_workspace_bytes(int64_t M, int64_t K, int64_t I, int64_t E, int64_t t
 int launch_moe_mlp(const MoeArgs& a, bool ue8m0, cudaStream_t stream) {
   DeviceInfo dev;
   if (int st = current_device_info(&dev)) return st;
-  const int64_t pairs = static_cast<int64_t>(a.M) * a.top_k;
-  const int64_t act = a.E < pairs ? a.E : pairs;
+  const int pairs = a.M * a.top_k;
   const Workspace w = carve(a.workspace, a.M, a.K, a.I, a.E, a.top_k);
-  alignas(64) CUtensorMap twg, twd, txa, txh;
-  if (int st = encode_tmap_2d_u8(&twg, a.qg, a.K, static_cast<uint64_t>(a.E) * 2 * a.I, a.K, 128,
+  alignas(64) CUtensorMap maps[4];   // gate+up, down, tokens, h
+  if (int st = encode_tmap_2d_u8(&maps[0], a.qg, a.K, static_cast<uint64_t>(a.E) * 2 * a.I, a.K,
+                                 128, 128, kSwizzle128B))
+    return st;
+  if (int st = encode_tmap_2d_u8(&maps[1], a.qd, a.I, static_cast<uint64_t>(a.E) * a.K, a.I, 128,
                                  128, kSwizzle128B))
     return st;
-  if (int st = encode_tmap_2d_u8(&twd, a.qd, a.I, static_cast<uint64_t>(a.E) * a.K, a.I, 128, 128,
-                                 kSwizzle128B))
+  if (int st = encode_tmap_2d_u8(&maps[2], a.qa, a.K, a.M, a.K, 128, 1, kSwizzle128B)) return st;
+  if (int st = encode_tmap_2d_u8(&maps[3], w.qh, a.I, pairs, a.I, 128, 16, kSwizzle128B))
     return st;
-  if (int st = encode_tmap_2d_u8(&txa, a.qa, a.K, a.M, a.K, 128, 1, kSwizzle128B)) return st;
-  if (int st = encode_tmap_2d_u8(&txh, w.qh, a.I, pairs, a.I, 128, 16, kSwizzle128B)) return st;
 
+  const Layout lay(pairs, a.M <= 16 ? 16 : a.M <= 32 ? 32 : 64);
+  MlpArgs g{};
+  g.plan = w.plan;
+  g.shape.M = a.M;
+  g.shape.K = a.K;
+  g.shape.I = a.I;
+  g.shape.top_k = a.top_k;
+  g.shape.sms = dev.sm_count;
+  g.shape.room = lay.room();
+  g.shape.cap_gu = w.cap_gu;
+  g.shape.cap_down = w.cap_down;
+  g.shape.y_items = a.M < 4 ? 1 : a.M / 4;   // at most 32 tasks share 128 columns
+  g.shape.y_tasks = (4 * a.M + g.shape.y_items - 1) / g.shape.y_items;
+  g.sa = a.sa;
+  g.sg = a.sg;
+  g.sd = a.sd;
+  g.qh = w.qh;
+  g.sh = w.sh;
+  g.y = a.y;
+  g.part_gu = w.part_gu;
+  g.part_down = w.part_down;
+  g.off_row = lay.off_row;
+  g.off_w = lay.off_w;
+  g.off_tab = lay.off_tab;
+  g.off_tiles = lay.off_tiles;
+  g.wait_limit = a.wait_limit;
+  g.err = a.err;
+
+  // a thread for each expert; more where there are more choices
+  const int want = a.E > pairs ? a.E : pairs;
+  const int threads = want < 256 ? 256 : want < kPlanThreads ? (want + 31) / 32 * 32 : kPlanThreads;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(1, 1, 1);
-  cfg.blockDim = dim3(kPlanThreads, 1, 1);
+  cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
   cfg.stream = stream;
   cudaLaunchAttribute pdl;
   pdl.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   pdl.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &pdl;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, moe_plan_kernel, a.ids, a.weights, static_cast<int>(pairs), a.top_k,
-                         a.E, a.first_expert, static_cast<int>(act * (a.I / 128)), a.K / 128,
-                         w.plan) != cudaSuccess)
+  if (cudaLaunchKernelEx(&cfg, moe_plan_kernel, a.ids, a.weights, pairs, a.E, a.first_expert,
+                         g.plan, g.shape) != cudaSuccess)
     return FP8BS_ERR_CUDA;
-
-  GemmMoeArgs g{};
-  g.plan = w.plan;
-  g.qh = w.qh;
-  g.sh = w.sh;
-  g.y = a.y;
-  g.partial = w.partial;
-  g.M = a.M;
-  g.K = a.K;
-  g.I = a.I;
-  g.wait_limit = a.wait_limit;
-  g.err = a.err;
-  const int grid = dev.sm_count < kMaxCtas ? dev.sm_count : kMaxCtas;
-  g.sx = a.sa;
-  g.sw = a.sg;
-  if (int st = ue8m0 ? launch_gemm_n<false, true>(twg, txa, g, grid, dev.device, stream)
-                     : launch_gemm_n<false, false>(twg, txa, g, grid, dev.device, stream))
-    return st;
-  g.sx = w.sh;
-  g.sw = a.sd;
-  return ue8m0 ? launch_gemm_n<true, true>(twd, txh, g, grid, dev.device, stream)
-               : launch_gemm_n<true, false>(twd, txh, g, grid, dev.device, stream);
+  return ue8m0 ? launch_mlp_n<true>(maps, g, dev.device, stream)
+               : launch_mlp_n<false>(maps, g, dev.device, stream);
 }
 
 }  // namespace fp8bs

@@ -265,3 +265,35 @@ def test_refusals():
         fb.fp8_moe_mlp(*rep, *big[4:])
     y = fb.fp8_moe_mlp(qa[:0], sa[:0], ids[:0], w[:0], qg, sg, qd, sd)
     assert y.shape == (0, 256)
+
+
+@pytest.mark.parametrize("M,K,I,E,k", [
+    (1, 512, 8192, 8, 8), (2, 256, 6272, 4, 3), (3, 4096, 384, 5, 5), (1, 8192, 128, 2, 1),
+    (128, 128, 128, 64, 32), (128, 256, 384, 1, 1), (97, 640, 384, 2, 1), (40, 256, 128, 1024, 4),
+    (128, 1024, 896, 3, 2), (64, 384, 2176, 2, 2)])
+def test_results_of_many_parts(M, K, I, E, k):
+    """Results summed from many chunks (long K or I with few tokens, more than
+    16 parts of an output), experts with two blocks of tokens, as many choices
+    and experts as there can be."""
+    args = _case(M, K, I, E, k, "fp32", seed=200 + M + I)
+    y = fb.fp8_moe_mlp(*args)
+    _check(y, args)
+    assert torch.equal(y, fb.fp8_moe_mlp(*args))
+
+
+@pytest.mark.parametrize("M", [1, 24, 128])
+def test_bounded_wait_reports_timeout_and_recovers(M):
+    """A wait limit of one cycle: the call records the timeout and ends, and the
+    next one with the default limit, on the same workspace, is right."""
+    args = _case(M, 1024, 512, 4, 2, "fp32", seed=81)
+    ws = torch.empty(fb.moe_workspace_bytes(M, 1024, 512, 4, 2), dtype=torch.uint8, device="cuda")
+    fb.get_device_error()
+    try:
+        fb.set_wait_limit(1)
+        fb.fp8_moe_mlp(*args, workspace=ws)
+        assert fb.get_device_error() == 6
+    finally:
+        fb.set_wait_limit(0)
+    y = fb.fp8_moe_mlp(*args, workspace=ws)
+    assert fb.get_device_error() == 0
+    _check(y, args)
