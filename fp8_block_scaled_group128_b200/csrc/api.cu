@@ -398,8 +398,10 @@ static int add_rmsnorm_quant(const void* x, const void* res, const void* w, floa
     return FP8BS_ERR_ALIGN;
   DeviceInfo dev;
   if (int st = current_device_info(&dev)) return st;
+  int* err = device_error_word();
+  if (err == nullptr) return FP8BS_ERR_CUDA;
   return from_cuda(launch_add_rmsnorm_quant(x, res, w, eps, M, K, res_out, y, q, s, ue8m0,
-                                            static_cast<cudaStream_t>(stream)));
+                                            wait_limit(), err, static_cast<cudaStream_t>(stream)));
 }
 
 int fp8_add_rmsnorm_quant(const void* x_bf16, const void* residual_bf16, const void* weight_bf16,

@@ -159,6 +159,17 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, u
       : "memory");
 }
 
+// Untiled bulk load global -> this CTA's shared memory; both addresses and the
+// size are multiples of 16 bytes.
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes,
+                                          uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          smem_u32(dst)),
+      "l"(src), "r"(bytes), "r"(smem_u32(bar))
+      : "memory");
+}
+
 // Gather of four rows of a 2-D tensor (box one row high): rows r0..r3, columns
 // from x on, land one after the other at dst. x times the element size must be
 // a multiple of 16 bytes; a row outside the tensor reads as zeros.
@@ -496,6 +507,18 @@ __device__ __forceinline__ void fma2(float& a0, float& a1, float x0, float x1, f
       "fma.rn.f32x2 a, x, s, a;\n\t"
       "mov.b64 {%0, %1}, a;\n\t}"
       : "+f"(a0), "+f"(a1)
+      : "f"(x0), "f"(x1), "f"(s0), "f"(s1));
+}
+
+// Two fp32 products in one instruction.
+__device__ __forceinline__ void mul2(float& p0, float& p1, float x0, float x1, float s0,
+                                     float s1) {
+  asm("{\n\t.reg .b64 p, x, s;\n\t"
+      "mov.b64 x, {%2, %3};\n\t"
+      "mov.b64 s, {%4, %5};\n\t"
+      "mul.rn.f32x2 p, x, s;\n\t"
+      "mov.b64 {%0, %1}, p;\n\t}"
+      : "=f"(p0), "=f"(p1)
       : "f"(x0), "f"(x1), "f"(s0), "f"(s1));
 }
 

@@ -83,7 +83,8 @@ int launch_sparse24_gemm(const void* qa, const float* sa, const void* vals, cons
 constexpr int64_t kNormMaxK = 65536;
 cudaError_t launch_add_rmsnorm_quant(const void* x, const void* res, const void* w, float eps,
                                      int64_t M, int64_t K, void* res_out, void* y, void* q,
-                                     void* s, bool ue8m0, cudaStream_t stream);
+                                     void* s, bool ue8m0, long long wait_limit, int* err,
+                                     cudaStream_t stream);
 
 // The router's choice of top_k of E experts per token and their weights.
 cudaError_t launch_moe_route(const void* logits, bool bf16, const float* bias, bool sigmoid,

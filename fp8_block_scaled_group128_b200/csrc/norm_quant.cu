@@ -11,8 +11,12 @@
 // keeps and later layers read. n stays in fp32: the codes are rounded once,
 // from n, and not from the bf16 y.
 //
-// Bound: HBM. A row is read once and held in registers as bf16 between the sum
-// of squares and the codes.
+// Bound: HBM; a row is read once. Few rows are held in registers (as bf16)
+// between the sum of squares and the codes, with as many threads as a row has
+// chunks: one row of 4096 2.1 us, 64 rows of 7168 3.2 us. Many rows go through
+// shared memory (norm_row_kernel).
+#include <mutex>
+
 #include "common.cuh"
 #include "e4m3_codec.cuh"
 #include "kernels.h"
@@ -43,6 +47,45 @@ __device__ __forceinline__ uint32_t bf16x2_of(float lo, float hi) {
 __device__ __forceinline__ uint32_t add_bf16x2(uint32_t a, uint32_t b) {
   return bf16x2_of(__uint_as_float(a << 16) + __uint_as_float(b << 16),
                    __uint_as_float(a & 0xFFFF0000u) + __uint_as_float(b & 0xFFFF0000u));
+}
+
+// The same in one instruction: rounding the sum at once gives the same value
+// (two bf16 values' sum is exact in fp32 unless the smaller one is too small to
+// move the larger).
+__device__ __forceinline__ uint32_t hadd_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// Largest magnitude, NaN if one is.
+__device__ __forceinline__ float absmax_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(fabsf(a)), "f"(fabsf(b)));
+  return r;
+}
+__device__ __forceinline__ float absmax_nan(float a, float b, float c) {
+  float r;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// Codes of eight values for a scale: x * (1 / s) with the reciprocal of the
+// hardware (one ulp), so that a quotient is off by less than two fp32 ulps. For
+// scales whose reciprocal is not a normal number, zero and NaN the IEEE
+// quotients.
+__device__ __forceinline__ uint2 encode8_by_reciprocal(const float (&x)[8], float s) {
+  if (!(s >= 7.88860905e-31f)) return encode8f(x, ScaleDivider(s));   // 2^-100
+  float inv;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
+  float q[8];
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) mul2(q[i], q[i + 1], x[i], x[i + 1], inv, inv);
+  const uint32_t a = __nv_cvt_float2_to_fp8x2(make_float2(q[0], q[1]), __NV_SATFINITE, __NV_E4M3);
+  const uint32_t b = __nv_cvt_float2_to_fp8x2(make_float2(q[2], q[3]), __NV_SATFINITE, __NV_E4M3);
+  const uint32_t c = __nv_cvt_float2_to_fp8x2(make_float2(q[4], q[5]), __NV_SATFINITE, __NV_E4M3);
+  const uint32_t d = __nv_cvt_float2_to_fp8x2(make_float2(q[6], q[7]), __NV_SATFINITE, __NV_E4M3);
+  return make_uint2(prmt(a, b, 0x5410u), prmt(c, d, 0x5410u));
 }
 
 __device__ __forceinline__ void unpack8(const uint4 v, float (&f)[8]) {
@@ -141,6 +184,161 @@ __global__ void __launch_bounds__(1024) norm_quant_kernel(const NormArgs a) {
   }
 }
 
+// ------------------------------------------------------------- many rows --
+// A block per row (or several short ones), the row in shared memory: one bulk
+// copy brings it, the first pass adds the residual and the squares, the second
+// makes the codes. A thread's registers hold one 16-byte chunk at a time, so
+// that enough blocks are resident to keep HBM busy while others compute.
+//
+// 8192 rows of 4096 with residual and y: 49.3 us, 93% of the copy bandwidth (in
+// registers: 53.7); 1037 rows of 14336, codes only: 15.6 us (in registers: 24.2),
+// bound by instructions there, about 20 for an element; 2048 rows of 7168: 26.0
+// (30.9). A persistent kernel whose teams of warps held their rows in registers
+// behind a ring of bulk copies took 59, 19.5 and 27 us.
+constexpr int kRowSmem = 100 * 1024;   // at least two blocks per SM
+constexpr int kRowThreads = 512;
+constexpr int64_t kManyRows = 149;
+
+struct RowArgs {
+  NormArgs n;
+  long long wait_limit;
+  int* err;
+};
+
+template <bool kE8, bool kRes>
+__global__ void __launch_bounds__(kRowThreads) norm_row_kernel(const RowArgs a) {
+  extern __shared__ __align__(128) uint8_t rows_smem[];
+  __shared__ uint64_t full;
+  __shared__ float red[32];
+  const int T = blockDim.x, t = threadIdx.x, lane = t & 31;
+  const int64_t m0 = static_cast<int64_t>(blockIdx.x) * blockDim.y;
+  const int rows = static_cast<int>(min(static_cast<int64_t>(blockDim.y), a.n.M - m0));
+  const bool first = t == 0 && threadIdx.y == 0;
+  if (first) {
+    mbar_init(&full, 1);
+    fence_mbarrier_init();
+  }
+  grid_dependency_wait();
+  grid_launch_dependents();
+  if (first) {
+    const uint32_t bytes = static_cast<uint32_t>(rows * a.n.chunks * 16);
+    mbar_arrive_expect_tx(&full, kRes ? 2 * bytes : bytes);
+    bulk_load(rows_smem, a.n.x + m0 * a.n.chunks, bytes, &full);
+    if constexpr (kRes)
+      bulk_load(rows_smem + blockDim.y * a.n.chunks * 16, a.n.res + m0 * a.n.chunks, bytes, &full);
+  }
+  // one warp polls for all: the others' polls would take half of the issue slots
+  const bool polls = t < 32 && threadIdx.y == 0;
+  __syncwarp();
+  if (!__syncthreads_and(!polls || mbar_wait(&full, 0, a.wait_limit))) {
+    if (first) {
+      record_device_error(a.err, FP8BS_ERR_DEVICE_TIMEOUT);
+      mbar_wait(&full, 0, kDefaultWaitCycles);   // the copy must have landed before the exit
+    }
+    return;
+  }
+  const int y = threadIdx.y;
+  const bool live = y < rows;
+  const int chunks = live ? a.n.chunks : 0;
+  const int64_t base = (m0 + y) * a.n.chunks;
+  uint4* row = reinterpret_cast<uint4*>(rows_smem) + y * a.n.chunks;
+  const uint4* res = row + blockDim.y * a.n.chunks;
+  float s0 = 0.0f, s1 = 0.0f;
+#pragma unroll 1
+  for (int c = t; c < chunks; c += T) {
+    uint4 r = row[c];
+    if constexpr (kRes) {
+      const uint4 b = res[c];
+      r = make_uint4(hadd_bf16x2(r.x, b.x), hadd_bf16x2(r.y, b.y), hadd_bf16x2(r.z, b.z),
+                     hadd_bf16x2(r.w, b.w));
+      row[c] = r;
+      if (a.n.res_out != nullptr) a.n.res_out[base + c] = r;
+    }
+    float f[8];
+    unpack8(r, f);
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) fma2(s0, s1, f[i], f[i + 1], f[i], f[i + 1]);
+  }
+  float sum = s0 + s1;
+#pragma unroll
+  for (int off = 16; off >= 1; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+  if (T > 32) {
+    const int warps = T >> 5;
+    float* mine = red + y * warps;
+    if (lane == 0) mine[t >> 5] = sum;
+    __syncthreads();
+    sum = lane < warps ? mine[lane] : 0.0f;
+#pragma unroll
+    for (int off = 8; off >= 1; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+    sum = __shfl_sync(0xffffffffu, sum, 0);
+  }
+  const float rstd = __frsqrt_rn(fmaf(sum, a.n.inv_k, a.n.eps));
+  // a thread reads the chunks that it wrote; T is a multiple of 16, so that 16
+  // neighbouring threads have a group of 128 (all or none of them)
+#pragma unroll 1
+  for (int c = t; c < (chunks + 31) / 32 * 32; c += T) {
+    const bool on = c < chunks;
+    float n[8], w[8];
+    unpack8(on ? row[c] : make_uint4(0u, 0u, 0u, 0u), n);
+    uint4 wv = make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);
+    if (a.n.w != nullptr && on) wv = __ldg(a.n.w + c);
+    unpack8(wv, w);
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+      mul2(n[i], n[i + 1], n[i], n[i + 1], rstd, rstd);
+      mul2(n[i], n[i + 1], n[i], n[i + 1], w[i], w[i + 1]);
+    }
+    if (on && a.n.y != nullptr)
+      a.n.y[base + c] = make_uint4(bf16x2_of(n[0], n[1]), bf16x2_of(n[2], n[3]),
+                                   bf16x2_of(n[4], n[5]), bf16x2_of(n[6], n[7]));
+    float mx = absmax_nan(absmax_nan(n[0], n[1], n[2]), absmax_nan(n[3], n[4], n[5]),
+                          absmax_nan(n[6], n[7]));
+#pragma unroll
+    for (int off = 8; off >= 1; off >>= 1)
+      mx = absmax_nan(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+    uint2 q;
+    if constexpr (kE8) {
+      const uint32_t code = ue8m0_code_of_amax(mx);
+      q = encode8f_pow2(n, ue8m0_inv_scale(code));
+      if (on && (t & 15) == 0)
+        static_cast<uint8_t*>(a.n.s)[(base + c) >> 4] = static_cast<uint8_t>(code);
+    } else {
+      const float sc = scale_of_amax(mx);
+      q = encode8_by_reciprocal(n, sc);
+      if (on && (t & 15) == 0) static_cast<float*>(a.n.s)[(base + c) >> 4] = sc;
+    }
+    if (on) a.n.q[base + c] = q;
+  }
+}
+
+template <bool kE8, bool kRes>
+cudaError_t launch_rows(const RowArgs& a, const DeviceInfo& dev, cudaStream_t stream) {
+  auto kern = norm_row_kernel<kE8, kRes>;
+  static std::once_flag flags[64];
+  cudaError_t attr_err = cudaSuccess;
+  std::call_once(flags[dev.device], [&] {
+    attr_err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kRowSmem);
+  });
+  if (attr_err != cudaSuccess) return attr_err;
+  // two chunks for a thread (8192 rows of 4096: 49.3 us, with four 51.1)
+  int T = ((a.n.chunks + 1) / 2 + 31) / 32 * 32;
+  if (T > kRowThreads) T = kRowThreads;
+  const int R = T >= 128 ? 1 : 128 / T;
+  const int64_t blocks = (a.n.M + R - 1) / R;
+  if (blocks > 0x7FFFFFFF) return cudaErrorInvalidValue;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks), 1, 1);
+  cfg.blockDim = dim3(static_cast<unsigned>(T), static_cast<unsigned>(R), 1);
+  cfg.dynamicSmemBytes = static_cast<size_t>(R) * a.n.chunks * (kRes ? 32 : 16);
+  cfg.stream = stream;
+  cudaLaunchAttribute pdl;
+  pdl.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  pdl.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &pdl;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, a);
+}
+
 template <bool kE8>
 cudaError_t launch_norm(const NormArgs& a, cudaStream_t stream) {
   // threads per row: one chunk each up to 1024 threads, then 2, 4 or 8 chunks
@@ -171,7 +369,8 @@ cudaError_t launch_norm(const NormArgs& a, cudaStream_t stream) {
 
 cudaError_t launch_add_rmsnorm_quant(const void* x, const void* res, const void* w, float eps,
                                      int64_t M, int64_t K, void* res_out, void* y, void* q,
-                                     void* s, bool ue8m0, cudaStream_t stream) {
+                                     void* s, bool ue8m0, long long wait_limit, int* err,
+                                     cudaStream_t stream) {
   NormArgs a;
   a.x = static_cast<const uint4*>(x);
   a.res = static_cast<const uint4*>(res);
@@ -184,6 +383,19 @@ cudaError_t launch_add_rmsnorm_quant(const void* x, const void* res, const void*
   a.chunks = static_cast<int>(K / 8);
   a.inv_k = 1.0f / static_cast<float>(K);
   a.eps = eps;
+  // more rows than SMs: the rows' latency no longer decides (150 rows of 7168: 4.6 us
+  // either way)
+  const bool many = K * (res != nullptr ? 4 : 2) <= kRowSmem && M >= kManyRows;
+  if (many) {
+    DeviceInfo dev;
+    if (current_device_info(&dev) != FP8BS_OK) return cudaErrorUnknown;
+    const RowArgs rows{a, wait_limit, err};
+    if (res != nullptr)
+      return ue8m0 ? launch_rows<true, true>(rows, dev, stream)
+                   : launch_rows<false, true>(rows, dev, stream);
+    return ue8m0 ? launch_rows<true, false>(rows, dev, stream)
+                 : launch_rows<false, false>(rows, dev, stream);
+  }
   return ue8m0 ? launch_norm<true>(a, stream) : launch_norm<false>(a, stream);
 }
 

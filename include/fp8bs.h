@@ -307,7 +307,9 @@ int fp8_gather_columns(const void* src_bf16, int64_t P, int64_t M, int64_t Np, v
  *   q_e4m3 [M][K], s [M][K/128] fp32 (the _ue8m0 form: codes, one byte each).
  *   eps >= 0 and finite.
  * The codes come from the fp32 n (not from y). They are those of e4m3(n / s)
- * except where n / s lies within an fp32 ulp of the middle between two codes.
+ * except where n / s lies within two fp32 ulps of the middle between two codes.
+ * M >= 149 takes another kernel than fewer rows: the same row can differ in such
+ * a code, and in the last bits of n, between the two.
  * K a positive multiple of 128, at most 65536. A row with a NaN, or an infinity,
  * gives NaN in the groups where n is NaN.
  */

@@ -189,3 +189,61 @@ def test_refusals():
         fb.fp8_add_rmsnorm_quant(x, eps=-1.0)
     empty = fb.fp8_add_rmsnorm_quant(x[:0], residual=res[:0], weight=w)
     assert empty[0].shape == (0, 512)
+
+
+@pytest.mark.parametrize("fmt", FMT)
+@pytest.mark.parametrize("with_res", [True, False])
+@pytest.mark.parametrize("M,K", [(149, 128), (150, 256), (701, 384), (1000, 1920), (149, 14336),
+                                 (200, 25600), (149, 28672), (160, 51200)])
+def test_many_rows(M, K, with_res, fmt):
+    """The kernel for many rows: short rows that share a block (the last one
+    in part), rows up to its shared memory and beyond."""
+    x, res, w = _inputs(M, K, seed=3 * M + K)
+    res = res if with_res else None
+    q, s, y, r = _fn(fmt)(x, residual=res, weight=w, eps=EPS)
+    n, r_ref = ref.norm_rows(x, res, w, EPS)
+    assert r is None if res is None else torch.equal(r, r_ref)
+    ref.check_norm(n, fmt, q, s, y)
+    q2, s2, y2, _ = _fn(fmt)(x, residual=res, weight=w, eps=EPS, want_y=False)
+    assert y2 is None and torch.equal(q, q2) and torch.equal(s, s2)
+
+
+@pytest.mark.parametrize("fmt", FMT)
+def test_many_rows_with_unusual_values(fmt):
+    """Zeros, NaN, infinities and weights of 2^-110 (scales whose reciprocal is
+    not used) among ordinary rows; the addition in place."""
+    x, res, w = _inputs(300, 640, seed=20)
+    w[128:256] = 2.0 ** -110
+    res[7] = 0
+    x[7] = 0
+    x[11, 300:] = 0
+    res[11, 300:] = -0.0
+    x[20, 5] = float("nan")
+    x[30, 639] = float("inf")
+    ro = res.clone()
+    q, s, y, r = _fn(fmt)(x, residual=ro, weight=w, eps=EPS, residual_out=ro)
+    n, r_ref = ref.norm_rows(x, res, w, EPS)
+    keep = torch.tensor([i for i in range(300) if i not in (20, 30)], device="cuda")
+    assert r.data_ptr() == ro.data_ptr() and torch.equal(r[keep], r_ref[keep])
+    ref.check_norm(n[keep], fmt, q[keep], s[keep], y[keep])
+    assert bool((q[7] == 0).all()) and bool((q[11, 384:] == 0).all())
+    assert bool(y[20].isnan().all()) and bool(((q[20] & 0x7F) == 0x7F).all())
+    assert bool(y[30, 639].isnan()) and bool((y[30, :512] == 0).all())
+    few = _fn(fmt)(x[:40], residual=res[:40], weight=w, eps=EPS)
+    assert torch.equal(few[3][:20], r[:20])
+
+
+def test_many_rows_timeout_is_reported():
+    """A wait limit of one cycle: the error is recorded, the next call is right."""
+    x, res, w = _inputs(400, 4096, seed=21)
+    want = fb.fp8_add_rmsnorm_quant(x, residual=res, weight=w)
+    fb.get_device_error()
+    try:
+        fb.set_wait_limit(1)
+        fb.fp8_add_rmsnorm_quant(x, residual=res, weight=w)
+        assert fb.get_device_error() == 6
+    finally:
+        fb.set_wait_limit(0)
+    for a, b in zip(fb.fp8_add_rmsnorm_quant(x, residual=res, weight=w), want):
+        assert torch.equal(a, b)
+    assert fb.get_device_error() == 0
