@@ -23,7 +23,8 @@ namespace fp8bs {
 
 namespace {
 
-constexpr int kWarps = 4;   // rows per block, one warp each
+constexpr int kWarps = 4;         // warps of a block where there are many rows
+constexpr int kFewRows = 592;     // four per SM
 
 struct RouteArgs {
   const void* logits;
@@ -33,6 +34,8 @@ struct RouteArgs {
   int64_t M;
   int E, top_k, n_group, topk_group;
   int bf16, sigmoid, renorm;
+  int lg_lanes;   // log2 of the lanes that scan a group
+  int per_inv;    // ceil(2^20 / experts of a group)
   float scale;
 };
 
@@ -46,6 +49,10 @@ __device__ __forceinline__ uint64_t ordered(double v) {
   return (b >> 63) ? ~b : (b | (1ull << 63));
 }
 
+__device__ __forceinline__ float unordered(uint32_t k) {
+  return __uint_as_float((k & 0x80000000u) ? k & 0x7FFFFFFFu : ~k);
+}
+
 // Largest key of the warp; every lane gets it.
 __device__ __forceinline__ uint32_t warp_max(uint32_t k) { return __reduce_max_sync(0xffffffffu, k); }
 __device__ __forceinline__ uint64_t warp_max(uint64_t k) {
@@ -57,115 +64,178 @@ __device__ __forceinline__ uint64_t warp_max(uint64_t k) {
 
 __device__ __forceinline__ float sigmoid32(float x) { return 1.0f / (1.0f + expf(-x)); }
 
-// Lane l of a row's warp holds the experts l, l + 32, ... (kPer of them). A
-// key of 0 stands for "not eligible": every ordered finite value is above it.
-template <int kPer, bool kScore>
-__global__ void __launch_bounds__(32 * kWarps) route_kernel(const RouteArgs a) {
+// sigmoid(x) in double precision for -60 <= x <= 60 without a branch, so that
+// the experts of a lane overlap (above 60 it is 1 to 2^-86): e^-x = 2^n e^r with r = -x - n ln 2 (ln 2 in two
+// parts, Cody and Waite), e^r by its Taylor series to r^13 (|r| <= ln 2 / 2:
+// the rest is below 2^-57), and 1 / (1 + e^-x) by two Newton steps from an fp32
+// reciprocal.
+__device__ __forceinline__ double sigmoid64(double x) {
+  const double magic = 6755399441055744.0;             // 1.5 * 2^52: rounds to an integer
+  const double t = fma(-x, 1.4426950408889634, magic);
+  const double n = t - magic;
+  double r = fma(n, -6.93147180369123816490e-01, -x);
+  r = fma(n, -1.90821492927058770002e-10, r);
+  double p = 1.0 / 6227020800.0;
+  p = fma(p, r, 1.0 / 479001600.0);
+  p = fma(p, r, 1.0 / 39916800.0);
+  p = fma(p, r, 1.0 / 3628800.0);
+  p = fma(p, r, 1.0 / 362880.0);
+  p = fma(p, r, 1.0 / 40320.0);
+  p = fma(p, r, 1.0 / 5040.0);
+  p = fma(p, r, 1.0 / 720.0);
+  p = fma(p, r, 1.0 / 120.0);
+  p = fma(p, r, 1.0 / 24.0);
+  p = fma(p, r, 1.0 / 6.0);
+  p = fma(p, r, 0.5);
+  p = fma(p, r, 1.0);
+  p = fma(p, r, 1.0);
+  const double e = __hiloint2double(__double2hiint(p) + (__double2loint(t) << 20), __double2loint(p));
+  const double d = 1.0 + e;
+  double q = static_cast<double>(__frcp_rn(static_cast<float>(d)));
+  q = fma(q, fma(-d, q, 1.0), q);
+  return fma(q, fma(-d, q, 1.0), q);
+}
+
+// The same for x < -60: e^x (1 + e^x is 1 there, to 2^-86).
+__device__ __noinline__ double sigmoid64_low(double x) { return exp(x); }
+
+// A row belongs to blockDim.x threads, which leave the experts' keys in shared
+// memory; the first of their warps chooses. Lane l of it answers for the experts
+// l, l + 32, ... and keeps the best of them. A key of 0 stands for "not
+// eligible": every ordered finite value is above it. The loops stay rolled: one
+// row's time goes mostly into fetching code.
+template <bool kScore>
+__global__ void __launch_bounds__(1024) route_kernel(const RouteArgs a) {
   using Key = typename std::conditional<kScore, uint64_t, uint32_t>::type;
-  extern __shared__ double group_keys[];   // [kWarps][E], with groups only
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t m = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
+  extern __shared__ uint64_t smem[];   // [blockDim.y][E] keys
+  const int lane = threadIdx.x & 31;
+  const int64_t m = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
   grid_dependency_wait();
   grid_launch_dependents();
-  if (m >= a.M) return;
+  const bool live = m < a.M;
   const float ninf = __uint_as_float(0xFF800000u);
-  float x[kPer];
-  Key key[kPer];
-  double* gk = group_keys + static_cast<int64_t>(warp) * a.E;
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int e = lane + 32 * i;
-    x[i] = ninf;
-    if (e < a.E)
-      x[i] = a.bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(a.logits)[m * a.E + e])
-                    : static_cast<const float*>(a.logits)[m * a.E + e];
-    const bool live = x[i] > ninf;   // false for NaN too
-    if (!live) x[i] = ninf;
-    if constexpr (kScore) {
-      double k = 1.0 / (1.0 + exp(-static_cast<double>(x[i])));
-      if (a.bias != nullptr && e < a.E) k += static_cast<double>(a.bias[e]);
-      key[i] = live && k > -HUGE_VAL ? ordered(k) : 0u;
-      if (a.n_group > 1 && e < a.E) gk[e] = key[i] ? k : -HUGE_VAL;
-    } else {
-      key[i] = live ? ordered(x[i]) : 0u;
+  const int E = a.E;
+  Key* keys = reinterpret_cast<Key*>(smem) + threadIdx.y * E;
+  const int64_t row = m * E;
+  auto logit = [&](int e) {
+    return a.bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(a.logits)[row + e])
+                  : static_cast<const float*>(a.logits)[row + e];
+  };
+  if (live) {
+#pragma unroll 2
+    for (int e = threadIdx.x; e < E; e += blockDim.x) {
+      const float x = logit(e);
+      const bool there = x > ninf;   // false for NaN too
+      if constexpr (kScore) {
+        double k = -HUGE_VAL;
+        if (there) k = x >= -60.0f ? sigmoid64(fminf(x, 60.0f)) : sigmoid64_low(x);
+        if (a.bias != nullptr) k += static_cast<double>(a.bias[e]);
+        reinterpret_cast<double*>(keys)[e] = there && k > -HUGE_VAL ? k : -HUGE_VAL;
+      } else {
+        keys[e] = there ? ordered(x) : 0u;
+      }
     }
   }
+  if (blockDim.x > 32) {
+    __syncthreads();
+  } else {
+    __syncwarp();
+  }
+  if (!live || threadIdx.x >= 32) return;
+  uint32_t open = 0xffffffffu;   // a bit for each group
   if constexpr (kScore) {
     if (a.n_group > 1) {
-      __syncwarp();
-      // lane g scores group g (n_group <= 32)
-      const int per = a.E / a.n_group;
+      // a group's two largest keys: L lanes each scan a part of it, then join
+      const double* gk = reinterpret_cast<const double*>(keys);
+      const int per = E / a.n_group, L = 1 << a.lg_lanes;
+      const int g = lane >> a.lg_lanes, part = lane & (L - 1);
       double first = -HUGE_VAL, second = -HUGE_VAL;
-      if (lane < a.n_group) {
-        for (int j = 0; j < per; ++j) {
-          const double k = gk[lane * per + j];
-          if (k > first) {
-            second = first;
-            first = k;
-          } else if (k > second) {
-            second = k;
-          }
+      if (g < a.n_group) {
+#pragma unroll 2
+        for (int j = part; j < per; j += L) {
+          const double v = gk[g * per + j];
+          const double low = v > first ? first : v;
+          first = v > first ? v : first;
+          second = low > second ? low : second;
         }
+      }
+#pragma unroll 1
+      for (int off = 1; off < L; off <<= 1) {
+        const double f = __shfl_xor_sync(0xffffffffu, first, off);
+        const double s = __shfl_xor_sync(0xffffffffu, second, off);
+        const double low = f > first ? first : f;
+        first = f > first ? f : first;
+        second = s > second ? s : second;
+        second = low > second ? low : second;
       }
       const double total = second > -HUGE_VAL ? first + second : first;
       int ahead = 0;   // groups before this one in the order of the scores
-      for (int g = 0; g < a.n_group; ++g) {
-        const double other = __shfl_sync(0xffffffffu, total, g);
-        ahead += (other > total || (other == total && g < lane)) ? 1 : 0;
+#pragma unroll 2
+      for (int o = 0; o < a.n_group; ++o) {
+        const double other = __shfl_sync(0xffffffffu, total, o << a.lg_lanes);
+        ahead += (other > total || (other == total && o < g)) ? 1 : 0;
       }
-      const uint32_t open =
-          __ballot_sync(0xffffffffu, lane < a.n_group && ahead < a.topk_group);
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        const int e = lane + 32 * i;
-        if (e < a.E && !((open >> (e / per)) & 1u)) key[i] = 0u;
-      }
+      // lane l answers for group l from here on
+      const int ahead_l = __shfl_sync(0xffffffffu, ahead, (lane << a.lg_lanes) & 31);
+      open = __ballot_sync(0xffffffffu, lane < a.n_group && ahead_l < a.topk_group);
     }
   }
-  // softmax over all experts
+  Key best = 0u;
+  int best_e = 0;
+#pragma unroll 2
+  for (int e = lane; e < E; e += 32) {
+    Key key;
+    if constexpr (kScore) {
+      const double k = reinterpret_cast<const double*>(keys)[e];
+      const bool in = (open >> ((e * a.per_inv) >> 20)) & 1u;   // group e / (E / n_group)
+      key = in && k > -HUGE_VAL ? ordered(k) : 0u;
+      keys[e] = key;
+    } else {
+      key = keys[e];
+    }
+    if (key > best) {
+      best = key;
+      best_e = e;
+    }
+  }
+  __syncwarp();
+  // softmax over all experts (never with scores: the keys are the logits)
   float top = ninf, sum = 0.0f;
-  if (!a.sigmoid) {
+  if constexpr (!kScore) {
+    if (!a.sigmoid) {
+      const uint32_t t = __reduce_max_sync(0xffffffffu, best);
+      top = t == 0u ? ninf : unordered(t);
+#pragma unroll 2
+      for (int e = lane; e < E; e += 32)
+        if (keys[e] != 0u) sum += expf(unordered(keys[e]) - top);
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) top = fmaxf(top, x[i]);
-#pragma unroll
-    for (int off = 16; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-    if (top > ninf) {
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) sum += expf(x[i] - top);
+      for (int off = 16; off >= 1; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
     }
-#pragma unroll
-    for (int off = 16; off >= 1; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
   }
-  // top_k times the largest key left; lane j keeps choice j (top_k <= 32)
+  // top_k times the largest key left; lane j keeps choice j (top_k <= 32). The
+  // whole warp looks for the next best key of the lane that lost one.
   int my_id = -1;
-  float my_w = 0.0f;
+#pragma unroll 1
   for (int j = 0; j < a.top_k; ++j) {
-    Key best = 0u;
-    int at = 0;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      if (key[i] > best) {
-        best = key[i];
-        at = i;
-      }
-    }
     const Key all = warp_max(best);
     if (all == 0u) break;
-    const uint32_t e = best == all ? static_cast<uint32_t>(lane + 32 * at) : 0xFFFFFFFFu;
-    const uint32_t id = __reduce_min_sync(0xffffffffu, e);
-    float xv = 0.0f;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      if (static_cast<uint32_t>(lane + 32 * i) == id) {
-        key[i] = 0u;
-        xv = x[i];
-      }
+    const int id = __reduce_min_sync(0xffffffffu, best == all ? best_e : 0x7FFFFFFF);
+    if (lane == j) my_id = id;
+    if (j == a.top_k - 1) break;
+    const int e = (id & 31) + 32 * lane;
+    const Key left = e != id && e < E ? keys[e] : 0u;
+    if (e == id) keys[id] = 0u;   // only this lane reads it
+    const Key next = warp_max(left);
+    const int next_e = __reduce_min_sync(0xffffffffu, left == next ? e : 0x7FFFFFFF);
+    if (lane == (id & 31)) {
+      best = next;
+      best_e = next_e;
     }
-    xv = __shfl_sync(0xffffffffu, xv, static_cast<int>(id & 31u));
-    if (lane == j) {
-      my_id = static_cast<int>(id);
-      my_w = a.sigmoid ? sigmoid32(xv) : expf(xv - top) / sum;
-    }
+  }
+  float my_w = 0.0f;
+  if (my_id >= 0) {
+    const float x = logit(my_id);
+    my_w = a.sigmoid ? sigmoid32(x) : expf(x - top) / sum;
   }
   if (a.renorm) {
     float total = my_w;
@@ -179,23 +249,28 @@ __global__ void __launch_bounds__(32 * kWarps) route_kernel(const RouteArgs a) {
   }
 }
 
-template <int kPer>
-cudaError_t launch_route(const RouteArgs& a, bool score, cudaStream_t stream) {
-  const int64_t blocks = (a.M + kWarps - 1) / kWarps;
+template <bool kScore>
+cudaError_t launch_route(const RouteArgs& a, cudaStream_t stream) {
+  // few rows: a thread for each expert (one row of 256: 4.1 us, with a warp 6.9);
+  // many: one or two warps for a row (4096 rows of 256: 11.1 us with two, 12.2 with
+  // one, 13.5 with eight)
+  const bool few = a.M <= kFewRows;
+  const int T = few ? (a.E + 31) / 32 * 32 : a.E > 64 ? 64 : 32;
+  const int R = few ? 1 : 32 * kWarps / T;
+  const int64_t blocks = (a.M + R - 1) / R;
   if (blocks > 0x7FFFFFFF) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(blocks), 1, 1);
-  cfg.blockDim = dim3(32 * kWarps, 1, 1);
+  cfg.blockDim = dim3(static_cast<unsigned>(T), static_cast<unsigned>(R), 1);
   // at most 4 x 1024 x 8 bytes
-  cfg.dynamicSmemBytes = a.n_group > 1 ? sizeof(double) * kWarps * static_cast<size_t>(a.E) : 0;
+  cfg.dynamicSmemBytes = (kScore ? 8 : 4) * R * static_cast<size_t>(a.E);
   cfg.stream = stream;
   cudaLaunchAttribute pdl;
   pdl.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   pdl.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &pdl;
   cfg.numAttrs = 1;
-  return score ? cudaLaunchKernelEx(&cfg, route_kernel<kPer, true>, a)
-               : cudaLaunchKernelEx(&cfg, route_kernel<kPer, false>, a);
+  return cudaLaunchKernelEx(&cfg, route_kernel<kScore>, a);
 }
 
 }  // namespace
@@ -218,13 +293,12 @@ cudaError_t launch_moe_route(const void* logits, bool bf16, const float* bias, b
   a.sigmoid = sigmoid;
   a.renorm = renorm;
   a.scale = scale;
-  const bool score = bias != nullptr || n_group > 1;
-  if (E <= 32) return launch_route<1>(a, score, stream);
-  if (E <= 64) return launch_route<2>(a, score, stream);
-  if (E <= 128) return launch_route<4>(a, score, stream);
-  if (E <= 256) return launch_route<8>(a, score, stream);
-  if (E <= 512) return launch_route<16>(a, score, stream);
-  return launch_route<32>(a, score, stream);
+  a.lg_lanes = 0;
+  while ((2 << a.lg_lanes) * n_group <= 32) ++a.lg_lanes;
+  const int per = static_cast<int>(E / n_group);
+  a.per_inv = ((1 << 20) + per - 1) / per;   // exact quotients for e < 1024
+  return bias != nullptr || n_group > 1 ? launch_route<true>(a, stream)
+                                        : launch_route<false>(a, stream);
 }
 
 }  // namespace fp8bs

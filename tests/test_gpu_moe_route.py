@@ -166,3 +166,34 @@ def test_refusals():
     with pytest.raises(ValueError):
         fb.moe_route_topk(x, 2, ids=torch.zeros(3, 3, dtype=torch.int32, device="cuda"))
     assert fb.moe_route_topk(x[:0], 2)[0].shape == (0, 2)
+
+
+@pytest.mark.parametrize("M", [5, 700])
+@pytest.mark.parametrize("E,ng,kg,k", [(48, 1, 1, 3), (48, 6, 2, 3), (200, 8, 3, 7), (1024, 32, 5, 9)])
+def test_few_and_many_rows(M, E, ng, kg, k):
+    """A thread for each expert, or one or two warps for a row; bf16 logits,
+    which tie; the weights of one are those of the other."""
+    x = _logits(M, E, seed=E + M, dtype=torch.bfloat16)
+    kw = dict(scoring="sigmoid", n_group=ng, topk_group=kg, bias=_bias(E, ng))
+    _check(x, k, **kw)
+    ids, w = fb.moe_route_topk(x, k, **kw)
+    more = fb.moe_route_topk(torch.cat([x, x]), k, **kw)
+    assert torch.equal(more[0][:M], ids) and torch.equal(more[1][M:], w)
+
+
+@pytest.mark.parametrize("ng,kg", [(1, 1), (4, 2)])
+def test_scores_far_from_zero(ng, kg):
+    """Logits down to -700 and up to the largest: scores near 0 and equal to 1."""
+    g = torch.Generator().manual_seed(12)
+    x = (torch.randn(20, 32, generator=g) * 150).clamp(-690, 1e4)
+    x[3] = -80 - 3 * torch.arange(32)
+    x[4, :20] = 50 + torch.arange(20)          # 1 in 64 bits: ties
+    x[5, 7] = 3e38
+    x[6] = torch.linspace(-61, -59, 32)
+    bias = torch.zeros(32, device="cuda")
+    _check_ids(x.cuda(), 6, scoring="sigmoid", bias=bias, n_group=ng, topk_group=kg)
+
+
+def _check_ids(x, k, **kw):
+    ids, _ = fb.moe_route_topk(x, k, **kw)
+    np.testing.assert_array_equal(ids.cpu().numpy(), ref.route(x, k, **kw)[0])
