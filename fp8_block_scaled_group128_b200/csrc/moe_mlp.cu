@@ -96,7 +96,7 @@ struct alignas(16) Head {
   int n_gu, total;      // chunks of gate+up; of both
   int groups;           // h tasks of a gate+up result
   int n_h, n_tasks;     // h tasks; of both kinds
-  int pad;
+  int top;              // rows of a token, at most
 };
 
 // What is known before the plan.
@@ -124,7 +124,8 @@ __host__ __device__ inline int chunks_of(int units, int depth, int sms, int most
   return n < 1 ? 1 : n;
 }
 
-__host__ __device__ inline Head cut_work(int blocks, int rows, int most, const Shape& s) {
+__host__ __device__ inline Head cut_work(int blocks, int rows, int most, int top,
+                                         const Shape& s) {
   const int KB = s.K / 128, IB = s.I / 128, DU = (IB + 1) / 2;
   Head h;
   h.blocks = blocks;
@@ -146,7 +147,7 @@ __host__ __device__ inline Head cut_work(int blocks, int rows, int most, const S
   h.groups = (most + kFinRows - 1) / kFinRows;
   h.n_h = blocks * IB * h.groups;
   h.n_tasks = h.n_h + KB * s.y_tasks;
-  h.pad = 0;
+  h.top = top;
   return h;
 }
 
@@ -232,8 +233,8 @@ struct Plan {
   int* ticket;       // [4]: chunks claimed; tasks claimed; h tasks complete; -
   int2* act;         // [blocks + 1]: (expert, its first row); the last entry ends the rows
   int* row_tok;      // [rows] token of a row
-  int* pair_row;     // [M][top_k] row of a choice, or -1
-  float* pair_w;     // [M][top_k] its weight
+  int* pair_row;     // [M][top_k] a token's rows in the order of its choices, then -1
+  float* pair_w;     // [M][top_k] their weights
   int* counters;     // zeroed:
   int* count_gu;     //   [blocks * I / 128] chunks written of a gate+up result
   int* count_down;   //   [K / 128] chunks written of a down result
@@ -300,13 +301,16 @@ __global__ void __launch_bounds__(kPlanThreads)
   __shared__ int expert[kMoeMaxM * kMoeMaxTopK];   // local expert of a choice, -1: none
   __shared__ float share[kMoeMaxM * kMoeMaxTopK];  // weight of a choice
   __shared__ int fill[kPlanThreads];               // next row of an expert
+  __shared__ uint8_t is_row[kMoeMaxM * kMoeMaxTopK];   // the token's first choice of this expert
   __shared__ uint32_t warp_sum[kPlanThreads / 32];
-  __shared__ int most;
+  __shared__ int token_rows[kMoeMaxM];
+  __shared__ int most, most_of_token;
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5, T = blockDim.x;
   const int top_k = shape.top_k;
   fill[t] = 0;
   if (t < kPlanThreads / 32) warp_sum[t] = 0u;
-  if (t == 0) most = 0;
+  if (t < kMoeMaxM) token_rows[t] = 0;
+  if (t == 0) most = most_of_token = 0;
   grid_dependency_wait();
   grid_launch_dependents();
 #pragma unroll 1
@@ -319,15 +323,17 @@ __global__ void __launch_bounds__(kPlanThreads)
   for (int i = t; i < plan.n_counters; i += T) plan.counters[i] = 0;
   if (t < 4) plan.ticket[t] = 0;
   __syncthreads();
-  auto is_row = [&](int i) {   // the token's first choice of this expert
-    if (expert[i] < 0) return false;
-    for (int j = i / top_k * top_k; j < i; ++j)
-      if (expert[j] == expert[i]) return false;
-    return true;
-  };
 #pragma unroll 1
-  for (int i = t; i < pairs; i += T)
-    if (is_row(i)) atomicAdd(&fill[expert[i]], 1);
+  for (int i = t; i < pairs; i += T) {
+    const int e = expert[i];
+    bool row = e >= 0;
+    for (int j = i / top_k * top_k; j < i; ++j) row &= expert[j] != e;
+    is_row[i] = row;
+    if (row) {
+      atomicAdd(&fill[e], 1);
+      atomicAdd(&token_rows[i / top_k], 1);
+    }
+  }
   __syncthreads();
   // exclusive prefix over the experts of (blocks << 16 | rows): at most 4096
   // rows, in at most 1024 + 63 blocks
@@ -344,6 +350,7 @@ __global__ void __launch_bounds__(kPlanThreads)
   // rows of the largest block (a block count of 1 or 2)
   const int top = __reduce_max_sync(0xffffffffu, blocks > 1 ? (n + 1) / 2 : n);
   if (lane == 0 && top > 0) atomicMax(&most, top);
+  if (t < shape.M) atomicMax(&most_of_token, token_rows[t]);
   __syncthreads();
   const uint32_t sums = warp_sum[lane];
   const uint32_t total = __reduce_add_sync(0xffffffffu, sums);
@@ -357,21 +364,26 @@ __global__ void __launch_bounds__(kPlanThreads)
   if (t == T - 1) {
     const int rows = static_cast<int>(total & 0xFFFFu);
     plan.act[total >> 16] = make_int2(-1, rows);
-    *plan.head = cut_work(static_cast<int>(total >> 16), rows, most, shape);
+    *plan.head = cut_work(static_cast<int>(total >> 16), rows, most, most_of_token, shape);
   }
 #pragma unroll 1
   for (int i = t; i < pairs; i += T) {
-    int row = -1;
+    const int first = i / top_k * top_k, end = first + top_k;
+    const int rows = token_rows[i / top_k];
+    int place = 0;   // rows of the token before this one
     float w = share[i];
-    if (is_row(i)) {
-      const int end = i / top_k * top_k + top_k;
-      for (int j = i + 1; j < end; ++j)
-        if (expert[j] == expert[i]) w += share[j];
-      row = atomicAdd(&fill[expert[i]], 1);
-      plan.row_tok[row] = i / top_k;
+#pragma unroll 2
+    for (int j = first; j < end; ++j) {
+      place += j < i && is_row[j];
+      if (j > i && expert[j] == expert[i]) w += share[j];
     }
-    plan.pair_row[i] = row;
-    plan.pair_w[i] = w;
+    if (is_row[i]) {
+      const int row = atomicAdd(&fill[expert[i]], 1);
+      plan.row_tok[row] = i / top_k;
+      plan.pair_row[first + place] = row;
+      plan.pair_w[first + place] = w;
+    }
+    if (i - first >= rows) plan.pair_row[i] = -1;
   }
 }
 
@@ -410,31 +422,26 @@ __device__ __forceinline__ void fence_proxy_async_all() {
   asm volatile("fence.proxy.async;" ::: "memory");
 }
 
-__device__ __forceinline__ int load_relaxed(const int* p) {
-  int v;
-  asm volatile("ld.relaxed.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
-  return v;
-}
-
-// Waits until *p >= target, for at most `limit` cycles; the whole warp. (Only
-// the last load acquires: an acquire empties the SM's L1.)
+// Waits until *p >= target, for at most `limit` cycles; the whole warp.
 __device__ __forceinline__ bool wait_count_warp(const int* p, int target, long long limit) {
   const long long t0 = clock64();
   bool ok = true;
-  while (load_relaxed(p) < target) {
+  while (load_acquire(p) < target) {
     if (clock64() - t0 > limit) {
       ok = false;
       break;
     }
     __nanosleep(100);
   }
-  return __all_sync(0xffffffffu, ok && load_acquire(p) >= target);
+  return __all_sync(0xffffffffu, ok);
 }
 
-// *p >= target now; the whole warp.
-__device__ __forceinline__ bool wait_now_warp(const int* p, int target) {
-  return __all_sync(0xffffffffu, load_relaxed(p) >= target) &&
-         __all_sync(0xffffffffu, load_acquire(p) >= target);
+__device__ __forceinline__ Head load_head(const Head* p) {
+  Head h;
+#pragma unroll
+  for (int i = 0; i < static_cast<int>(sizeof(Head)) / 16; ++i)
+    reinterpret_cast<int4*>(&h)[i] = __ldcg(reinterpret_cast<const int4*>(p) + i);
+  return h;
 }
 
 __device__ __forceinline__ void add4(float4& a, const float4& b) {
@@ -514,10 +521,7 @@ __global__ void __launch_bounds__(32 * (6 + kFin) + 128 * kWgs, 1)
   grid_launch_dependents();
   int ticket = 0;
   if (threadIdx.x == 0) ticket = atomicAdd(args.plan.ticket, 1);
-  Head head;
-#pragma unroll
-  for (int i = 0; i < static_cast<int>(sizeof(Head)) / 16; ++i)
-    reinterpret_cast<int4*>(&head)[i] = __ldcg(reinterpret_cast<const int4*>(args.plan.head) + i);
+  const Head head = load_head(args.plan.head);
   const int KB = args.shape.K / 128, IB = args.shape.I / 128;
   float* tab = reinterpret_cast<float*>(smem + args.off_tab);
   uint8_t* tiles = smem + args.off_tiles;
@@ -557,8 +561,11 @@ __global__ void __launch_bounds__(32 * (6 + kFin) + 128 * kWgs, 1)
   bool all_ready = false;
   auto wait_h = [&](const Chunk& ch) {
     if (all_ready) return true;
-    all_ready = wait_now_warp(h_done, head.n_h);
-    return all_ready || wait_count_warp(args.plan.ready + ch.ready, ch.needs, limit);
+    const bool all = load_acquire(h_done) >= head.n_h;
+    const bool some = load_acquire(args.plan.ready + ch.ready) >= ch.needs;
+    all_ready = __all_sync(0xffffffffu, all);
+    return __all_sync(0xffffffffu, all || some) ||
+           wait_count_warp(args.plan.ready + ch.ready, ch.needs, limit);
   };
 
   if (warp == 0) {
@@ -824,14 +831,18 @@ __global__ void __launch_bounds__(32 * (6 + kFin) + 128 * kWgs, 1)
     const int ncol = head.ncol;
     Ring tb, sb;
     bool ok = true;
-    Chunk ch;
     for (;;) {
-      const int slot = mr.i;
-      if (!next_chunk(ch, false)) break;
-      // this warpgroup's columns: [col0, col0 + cols)
-      const int per = (ch.n + 8 * kWgs - 1) / (8 * kWgs) * 8;
-      const int col0 = wg * per;
-      const int cols = max(0, min(per, (ch.n + 7) / 8 * 8 - col0));
+      int col0, cols, k, k1;
+      {
+        Chunk ch;
+        if (!next_chunk(ch, true)) break;
+        // this warpgroup's columns: [col0, col0 + cols)
+        const int per = (ch.n + 8 * kWgs - 1) / (8 * kWgs) * 8;
+        col0 = wg * per;
+        cols = max(0, min(per, (ch.n + 7) / 8 * 8 - col0));
+        k = 0;
+        k1 = ch.k1 - ch.k0;
+      }
       // the two products of the chunk's units times their scale products
       float acc[2][kPer];
 #pragma unroll
@@ -839,9 +850,9 @@ __global__ void __launch_bounds__(32 * (6 + kFin) + 128 * kWgs, 1)
 #pragma unroll
         for (int c = 0; c < kPer; ++c) acc[p][c] = 0.0f;
 #pragma unroll 1
-      for (int k = ch.k0; k < ch.k1; ++k) {
-        const int j = (k - ch.k0) % kBatch;
-        const bool batch_end = j == kBatch - 1 || k == ch.k1 - 1;
+      for (; k < k1; ++k) {
+        const int j = k % kBatch;
+        const bool batch_end = j == kBatch - 1 || k == k1 - 1;
         if (j == 0) ok = mbar_wait_warp(&bar.sfull[sb.i], sb.phase, limit);
         ok = ok && mbar_wait_warp(&bar.tfull[tb.i], tb.phase, limit);
         if (!ok) break;
@@ -876,26 +887,35 @@ __global__ void __launch_bounds__(32 * (6 + kFin) + 128 * kWgs, 1)
         tb.next(head.bufs);
       }
       if (!ok) break;
-      // gate+up: both values; down: their sum
+      // gate+up: both values; down: their sum. (The chunk is read again: the sums
+      // leave no registers to keep it.)
+      const Chunk& ch = sh.mail[mr.i];
       const bool down = ch.kind != 0;
-      const int64_t step = down ? args.shape.K : static_cast<int64_t>(IB) * 256;
+      const int64_t step = down ? args.shape.K : IB * 256;
       float* to = (down ? args.part_down + ch.tile * 128 : args.part_gu + ch.tile * 256) +
                   (static_cast<int64_t>(ch.c) * head.rows + ch.row0 + col0) * step + row;
+      const int mine = min(cols, ch.n - col0);
 #pragma unroll
-      for (int c = 0; c < kPer; ++c) {
-        if (col0 + c < ch.n && c < cols) {
-          __stcg(to + c * step, down ? acc[0][c] + acc[1][c] : acc[0][c]);
-          if (!down) __stcg(to + c * step + 128, acc[1][c]);
+      for (int c = 0; c < kPer; ++c, to += step) {
+        if (c < mine) {
+          __stcg(to, down ? acc[0][c] + acc[1][c] : acc[0][c]);
+          if (!down) __stcg(to + 128, acc[1][c]);
         }
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bar.dumped[slot]);
+      if (lane == 0) {
+        mbar_arrive(&bar.dumped[mr.i]);
+        mbar_arrive(&bar.mempty[mr.i]);
+      }
+      mr.next(kMail);
     }
     if (!ok) give_up();
     tc_fence_before();
   }
   if (warp >= 6) {
     // ------------------------------------------------------------ finishers --
+    // read again: the promotion warps have no registers to carry it
+    const Head head = load_head(args.plan.head);
     bool ok = true;
     int16_t* pair_row = reinterpret_cast<int16_t*>(smem + args.off_row);
     float* pair_w = reinterpret_cast<float*>(smem + args.off_w);
@@ -987,9 +1007,9 @@ __global__ void __launch_bounds__(32 * (6 + kFin) + 128 * kWgs, 1)
         if (!pairs_there) ok = mbar_wait_warp(&bar.pairs, 0, limit);
         if (!ok) break;
         pairs_there = true;
-        // part p: chunk p % cps of choice p / cps
-        const int parts = args.shape.top_k * head.cps;
-        const int lg = parts > 8 ? 4 : parts > 4 ? 3 : parts > 2 ? 2 : parts - 1;   // slots of an item
+        // part p: chunk p % cps of the token's row p / cps
+        const int parts = head.top * head.cps;
+        const int lg = parts > 8 ? 4 : parts > 4 ? 3 : parts > 2 ? 2 : parts > 1 ? 1 : 0;   // slots of an item
         const int grp = lane >> 3;
 #pragma unroll 1
         for (int it = item0; it < item1; it += 16 >> lg) {
@@ -1130,7 +1150,9 @@ int launch_moe_mlp(const MoeArgs& a, bool ue8m0, cudaStream_t stream) {
   g.shape.room = lay.room();
   g.shape.cap_gu = w.cap_gu;
   g.shape.cap_down = w.cap_down;
-  g.shape.y_items = a.M < 4 ? 1 : a.M / 4;   // at most 32 tasks share 128 columns
+  // one y task for each warp that can take one (promotion's too, by then)
+  const int y_all = 4 * a.M * (a.K / 128);
+  g.shape.y_items = (y_all + 10 * dev.sm_count - 1) / (10 * dev.sm_count);
   g.shape.y_tasks = (4 * a.M + g.shape.y_items - 1) / g.shape.y_items;
   g.sa = a.sa;
   g.sg = a.sg;
