@@ -434,20 +434,27 @@ def _norm_call(handle, dev, name, scale_dtype, x, residual, weight, eps, q, s, y
         rp = _operand(residual, bf16, shape, dev, "residual")
         if residual_out is None:
             residual_out = torch.empty_like(x)
-        op = _operand(residual_out, bf16, shape, dev, "residual_out")
+            op = residual_out.data_ptr()
+        else:
+            op = _operand(residual_out, bf16, shape, dev, "residual_out")
     elif residual_out is not None:
         raise ValueError("residual_out without a residual would be a copy of x")
-    if y is None and want_y:
-        y = torch.empty_like(x)
     if y is not None:
         yp = _operand(y, bf16, shape, dev, "y")
+    elif want_y:
+        y = torch.empty_like(x)
+        yp = y.data_ptr()
     if q is None:
         q = torch.empty_like(x, dtype=torch.uint8)
+        qp = q.data_ptr()
+    else:
+        qp = _operand(q, torch.uint8, shape, dev, "q")
     if s is None:
         s = x.new_empty(groups, dtype=scale_dtype)
-    st = getattr(lib(), name)(xp, rp, wp, eps, M, K, op, yp,
-                              _operand(q, torch.uint8, shape, dev, "q"),
-                              _operand(s, scale_dtype, groups, dev, "s"), handle)
+        sp = s.data_ptr()
+    else:
+        sp = _operand(s, scale_dtype, groups, dev, "s")
+    st = getattr(lib(), name)(xp, rp, wp, eps, M, K, op, yp, qp, sp, handle)
     if st:
         raise Fp8bsError(name, st)
     return q, s, y, residual_out
@@ -486,12 +493,16 @@ def _route_call(handle, dev, logits, top_k, scoring, bias, n_group, topk_group, 
     out = (M, max(top_k, 0))
     if ids is None:
         ids = logits.new_empty(out, dtype=torch.int32)
+        ip = ids.data_ptr()
+    else:
+        ip = _operand(ids, torch.int32, out, dev, "ids")
     if weights is None:
         weights = torch.empty_like(ids, dtype=torch.float32)
+        wp = weights.data_ptr()
+    else:
+        wp = _operand(weights, torch.float32, out, dev, "weights")
     st = lib().moe_route_topk(lp, dtype is torch.bfloat16, bp, ROUTE_SCORING[scoring], M, E, top_k,
-                              n_group, topk_group, bool(renormalize), scale,
-                              _operand(ids, torch.int32, out, dev, "ids"),
-                              _operand(weights, torch.float32, out, dev, "weights"), handle)
+                              n_group, topk_group, bool(renormalize), scale, ip, wp, handle)
     if st:
         raise Fp8bsError("moe_route_topk", st)
     return ids, weights
@@ -531,6 +542,9 @@ def _moe_call(handle, dev, name, scale_dtype, qa, sa, ids, weights, qg, sg, qd, 
             _operand(sd, scale_dtype, (E, KB, IB), dev, "sw_down"))
     if y is None:
         y = torch.empty_like(qa, dtype=torch.bfloat16)
+        yp = y.data_ptr()
+    else:
+        yp = _operand(y, torch.bfloat16, (M, K), dev, "y")
     if workspace is None:
         size = moe_workspace_bytes(M, K, I, E, top_k)
         workspace = qa.new_empty(size)
@@ -538,8 +552,8 @@ def _moe_call(handle, dev, name, scale_dtype, qa, sa, ids, weights, qg, sg, qd, 
         if _device_of(workspace, "workspace") != dev or not workspace.is_contiguous():
             raise ValueError("workspace must be a contiguous tensor on the operands' device")
         size = workspace.numel() * workspace.element_size()
-    st = getattr(lib(), name)(*args, _operand(y, torch.bfloat16, (M, K), dev, "y"), M, K, I, E,
-                              top_k, first_expert, workspace.data_ptr(), size, handle)
+    st = getattr(lib(), name)(*args, yp, M, K, I, E, top_k, first_expert, workspace.data_ptr(), size,
+                              handle)
     if st:
         raise Fp8bsError(name, st)
     return y

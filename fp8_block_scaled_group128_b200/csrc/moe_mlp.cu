@@ -261,10 +261,11 @@ Workspace carve(void* base, int64_t M, int64_t K, int64_t I, int64_t E, int64_t 
     at += (bytes + 255) / 256 * 256;
     return p;
   };
-  // as many parts as kPartFloats hold, from 1 to 64 where all choices are here
+  // what kPartFloats hold, from 1 to 64 parts where all choices are here (never
+  // less for more tokens: a workspace serves every smaller call)
   auto part_rows = [&](int64_t width) {
-    const int64_t parts = kPartFloats / (rows * width);
-    return static_cast<int>(rows * (parts < 1 ? 1 : parts > 64 ? 64 : parts));
+    const int64_t one = rows * width, most = 64 * one < kPartFloats ? 64 * one : kPartFloats;
+    return static_cast<int>((one > most ? one : most) / width);
   };
   Workspace w;
   w.plan.head = reinterpret_cast<Head*>(take(sizeof(Head)));
