@@ -113,20 +113,37 @@ struct Shape {
 // (they do not get equal bandwidth), but not below 8 units (one token through 2
 // experts of 4096 x 14336: 76 us with 4, 70 with 8, 72 with 16), nor below an
 // eighth of its tokens, where the partial sums weigh more than a quarter of the
-// weights. With less than 4 units for an SM, all SMs get some.
-__host__ __device__ inline int chunks_of(int units, int depth, int sms, int most, int cap) {
+// weights.
+struct Cut {
+  int q, n;   // units of a chunk; chunks of `depth` units
+};
+__host__ __device__ inline Cut cut_list(int units, int depth, int sms, int most, int cap) {
   const int each = (units + sms - 1) / sms;
-  int q = each < 4 ? each : each < 96 ? 8 : each / 12;
+  // (with less than 8 units for an SM at most 8 chunks, which the finishers
+  // load together)
+  const int few = (depth + 7) / 8;
+  int q = each < 8 ? (each > few ? each : few) : each < 96 ? 8 : each / 12;
   const int least = most < 8 ? 1 : (most + 7) / 8;
   if (q < least) q = least;
   int n = (depth + q / 2) / q;
   if (n > cap) n = cap;
-  return n < 1 ? 1 : n;
+  if (n < 1) n = 1;
+  Cut c;
+  c.q = (depth + n - 1) / n;
+  c.n = (depth + c.q - 1) / c.q;
+  return c;
 }
 
-__host__ __device__ inline Head cut_work(int blocks, int rows, int most, int top,
-                                         const Shape& s) {
+// The cut of gate+up (list 0) or down (list 1).
+__host__ __device__ inline Cut cut_of(int list, int blocks, int rows, int most, const Shape& s) {
   const int KB = s.K / 128, IB = s.I / 128, DU = (IB + 1) / 2;
+  return cut_list(blocks * KB * (list ? DU : IB), list ? DU : KB, s.sms, most,
+                  (list ? s.cap_down : s.cap_gu) / (rows < 1 ? 1 : rows));
+}
+
+__host__ __device__ inline Head head_of(int blocks, int rows, int most, int top, Cut gu, Cut down,
+                                        const Shape& s) {
+  const int KB = s.K / 128, IB = s.I / 128;
   Head h;
   h.blocks = blocks;
   h.rows = rows;
@@ -135,13 +152,10 @@ __host__ __device__ inline Head cut_work(int blocks, int rows, int most, int top
   h.stages = s.room / (kUnitBytes + 2 * h.xbytes);
   if (h.stages > kMaxStages) h.stages = kMaxStages;
   h.bufs = 256 / h.ncol;
-  const int r = rows < 1 ? 1 : rows;
-  h.cpt = chunks_of(blocks * IB * KB, KB, s.sms, most, s.cap_gu / r);
-  h.q_gu = (KB + h.cpt - 1) / h.cpt;
-  h.cpt = (KB + h.q_gu - 1) / h.q_gu;
-  h.cps = chunks_of(blocks * KB * DU, DU, s.sms, most, s.cap_down / r);
-  h.q_down = (DU + h.cps - 1) / h.cps;
-  h.cps = (DU + h.q_down - 1) / h.q_down;
+  h.q_gu = gu.q;
+  h.cpt = gu.n;
+  h.q_down = down.q;
+  h.cps = down.n;
   h.n_gu = blocks * IB * h.cpt;
   h.total = h.n_gu + blocks * h.cps * KB;
   h.groups = (most + kFinRows - 1) / kFinRows;
@@ -293,9 +307,68 @@ Workspace carve(void* base, int64_t M, int64_t K, int64_t I, int64_t E, int64_t 
 // -------------------------------------------------------------------- plan --
 // A choice counts once per token and expert: of a token's choices of the same
 // expert the first one makes the row and carries the sum of their weights (in
-// the order of the choices). The order of an expert's rows comes from atomics
-// and may differ from call to call; nothing computed depends on it. The block
-// has a thread for every expert at least, and two warps at least.
+// the order of the choices).
+
+// Up to 32 choices: one warp, a lane for each choice, without a barrier. The
+// blocks come in the order of the experts' first choices.
+__device__ __forceinline__ void plan_few(const int32_t* ids, const float* weights, int pairs, int E,
+                                         int first_expert, const Plan& plan, const Shape& shape) {
+  const int lane = threadIdx.x, top_k = shape.top_k;
+  int e = -1 - lane;   // no expert: like no other lane's
+  float w = 0.0f;
+  if (lane < pairs) {
+    const int64_t local = static_cast<int64_t>(ids[lane]) - first_expert;
+    w = weights[lane];
+    if (local >= 0 && local < E) e = static_cast<int>(local);
+  }
+  const uint32_t all = 0xffffffffu, before = (1u << lane) - 1u;
+  const int tok = lane / top_k, first = tok * top_k;
+  const uint32_t token = (top_k == 32 ? all : (1u << top_k) - 1u) << (first & 31);
+  const uint32_t same = __match_any_sync(all, e);
+  const bool row = e >= 0 && (same & token & before) == 0u;
+  for (int j = 0; j < top_k; ++j) {
+    const int from = (first + j) & 31;
+    const float other = __shfl_sync(all, w, from);
+    if (from > lane && ((same & token) >> from & 1u)) w += other;
+  }
+  const uint32_t rows = __ballot_sync(all, row);
+  const uint32_t mine = same & rows;                       // the expert's rows
+  const bool leads = row && (mine & before) == 0u;
+  const uint32_t leaders = __ballot_sync(all, leads);
+  const int n = row ? __popc(mine) : 0;
+  int scan = leads ? n : 0;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int o = __shfl_up_sync(all, scan, off);
+    if (lane >= off) scan += o;
+  }
+  const int row0 = __shfl_sync(all, scan - n, mine ? __ffs(static_cast<int>(mine)) - 1 : 0);
+  const int most = __reduce_max_sync(all, n);
+  const int of_token = lane < pairs ? __popc(rows & token) : 0;
+  const int top = __reduce_max_sync(all, of_token);
+  const int blocks = __popc(leaders), n_rows = __popc(rows);
+  // (lanes 0 and 1 are what counts)
+  const Cut c = cut_of(lane & 1, blocks, n_rows, most, shape);
+  Cut down;
+  down.q = __shfl_sync(all, c.q, 1);
+  down.n = __shfl_sync(all, c.n, 1);
+  if (lane == 0) {
+    *plan.head = head_of(blocks, n_rows, most, top, c, down, shape);
+    plan.act[blocks] = make_int2(-1, n_rows);
+  }
+  if (leads) plan.act[__popc(leaders & before)] = make_int2(e, row0);
+  if (row) {
+    const int r = row0 + __popc(mine & before), place = first + __popc(rows & token & before);
+    plan.row_tok[r] = tok;
+    plan.pair_row[place] = r;
+    plan.pair_w[place] = w;
+  }
+  if (lane < pairs && lane - first >= of_token) plan.pair_row[lane] = -1;
+}
+
+// The order of an expert's rows comes from atomics here and may differ from
+// call to call; nothing computed depends on it. The block has a thread for every
+// expert at least, and two warps at least.
 __global__ void __launch_bounds__(kPlanThreads)
     moe_plan_kernel(const int32_t* __restrict__ ids, const float* __restrict__ weights, int pairs,
                     int E, int first_expert, const Plan plan, const Shape shape) {
@@ -308,6 +381,18 @@ __global__ void __launch_bounds__(kPlanThreads)
   __shared__ int most, most_of_token;
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5, T = blockDim.x;
   const int top_k = shape.top_k;
+  if (pairs <= 32) {
+    grid_dependency_wait();
+    grid_launch_dependents();
+    if (warp == 0) {
+      plan_few(ids, weights, pairs, E, first_expert, plan, shape);
+    } else {
+      if (t < 36) plan.ticket[t - 32] = 0;
+#pragma unroll 1
+      for (int i = t - 32; i < plan.n_counters; i += T - 32) plan.counters[i] = 0;
+    }
+    return;
+  }
   fill[t] = 0;
   if (t < kPlanThreads / 32) warp_sum[t] = 0u;
   if (t < kMoeMaxM) token_rows[t] = 0;
@@ -362,10 +447,16 @@ __global__ void __launch_bounds__(kPlanThreads)
   if (blocks > 1) plan.act[(excl >> 16) + 1] = make_int2(t, row0 + n / 2);
   fill[t] = row0;
   __syncthreads();
-  if (t == T - 1) {
-    const int rows = static_cast<int>(total & 0xFFFFu);
-    plan.act[total >> 16] = make_int2(-1, rows);
-    *plan.head = cut_work(static_cast<int>(total >> 16), rows, most, most_of_token, shape);
+  if (warp == (T >> 5) - 1) {
+    const int rows = static_cast<int>(total & 0xFFFFu), n_blocks = static_cast<int>(total >> 16);
+    const Cut c = cut_of(lane & 1, n_blocks, rows, most, shape);
+    Cut down;
+    down.q = __shfl_sync(0xffffffffu, c.q, 1);
+    down.n = __shfl_sync(0xffffffffu, c.n, 1);
+    if (lane == 0) {
+      plan.act[n_blocks] = make_int2(-1, rows);
+      *plan.head = head_of(n_blocks, rows, most, most_of_token, c, down, shape);
+    }
   }
 #pragma unroll 1
   for (int i = t; i < pairs; i += T) {
@@ -693,7 +784,7 @@ __global__ void __launch_bounds__(32 * (6 + kFin) + 128 * kWgs, 1)
     // column's 8 scales lie next to each other in memory). The loads of a batch
     // (of its first columns) are under way before the buffer is waited for.
     const int j = lane & 7;
-    constexpr int kLoads = 4;
+    constexpr int kLoads = kN < 32 ? 4 : 8;
     Ring b;
     bool ok = true;
     Chunk ch;
@@ -705,16 +796,17 @@ __global__ void __launch_bounds__(32 * (6 + kFin) + 128 * kWgs, 1)
       const int64_t w0 =
           (static_cast<int64_t>(ch.expert) * (down ? KB : 2 * IB) + ch.tile) * kbs;
       const int64_t w1 = down ? 1 : static_cast<int64_t>(IB) * kbs;   // to the second tile's
-      const int x1 = down ? 1 : 0;
       bool waited = !down;
 #pragma unroll 1
       for (int k = ch.k0; k < ch.k1; k += kBatch, b.next(kTabs)) {
         if ((b.i & 1) != (warp == 4)) continue;
-        const int kb = down ? 2 * (k + j) : k + j;       // the unit's (first) K-block
-        const bool on = k + j < ch.k1;
-        const bool two = on && (!down || kb + 1 < kbs);
-        const float s0 = on ? scale_value(sw, w0 + kb, kE8) : 0.0f;
-        const float s1 = two ? scale_value(sw, w0 + kb + w1, kE8) : 0.0f;
+        // the unit's (first) K-block and its second one; what is behind the last
+        // unit or column is loaded from the last, so that no load has to wait for
+        // a branch
+        const int kb = min(down ? 2 * (k + j) : k + j, kbs - 1);
+        const bool two = !down || kb + 1 < kbs;
+        const float s0 = scale_value(sw, w0 + kb, kE8);
+        const float s1 = scale_value(sw, w0 + kb + (two ? w1 : 0), kE8);
         if (!waited) {
           ok = wait_h(ch);
           if (!ok) break;
@@ -723,17 +815,17 @@ __global__ void __launch_bounds__(32 * (6 + kFin) + 128 * kWgs, 1)
         float* out = tab + (b.i * kBatch + j) * tab_row;
 #pragma unroll 1
         for (int c0 = 0; c0 < ch.n; c0 += 4 * kLoads) {
+          int64_t at[kLoads];
           float v[kLoads], z[kLoads];
 #pragma unroll
           for (int i = 0; i < kLoads; ++i) {
-            const int c = c0 + (lane >> 3) + 4 * i;
-            v[i] = z[i] = 0.0f;
-            if (c < ch.n && on) {
-              const int64_t at =
-                  static_cast<int64_t>(down ? ch.row0 + c : row_tok[ch.row0 + c]) * kbs + kb;
-              v[i] = scale_value(sx, at, kE8);
-              if (two) z[i] = scale_value(sx, at + x1, kE8);
-            }
+            const int r = ch.row0 + min(c0 + (lane >> 3) + 4 * i, ch.n - 1);
+            at[i] = static_cast<int64_t>(down ? r : row_tok[r]) * kbs + kb;
+          }
+#pragma unroll
+          for (int i = 0; i < kLoads; ++i) {
+            v[i] = scale_value(sx, at[i], kE8);
+            z[i] = scale_value(sx, at[i] + (down && two ? 1 : 0), kE8);
           }
           if (c0 == 0) {
             ok = mbar_wait_warp(&bar.sempty[b.i], b.phase ^ 1u, limit);
@@ -744,7 +836,7 @@ __global__ void __launch_bounds__(32 * (6 + kFin) + 128 * kWgs, 1)
             const int c = c0 + (lane >> 3) + 4 * i;
             if (c < ch.n) {
               out[c] = v[i] * s0;
-              out[head.ncol + c] = z[i] * s1;
+              out[head.ncol + c] = two ? z[i] * s1 : 0.0f;
             }
           }
         }
@@ -930,6 +1022,7 @@ __global__ void __launch_bounds__(32 * (6 + kFin) + 128 * kWgs, 1)
       if (lane == 0) mbar_arrive(&bar.pairs);
     }
     bool pairs_there = false;
+    constexpr int kParts = 8;   // of a result, under way together
     const int64_t gu_row = static_cast<int64_t>(IB) * 256;   // floats of a row of part_gu
     while (!stopped()) {
       int task = 0;
@@ -952,10 +1045,10 @@ __global__ void __launch_bounds__(32 * (6 + kFin) + 128 * kWgs, 1)
           const int64_t part = head.rows * gu_row / 4;
           float4 g = make_float4(0.0f, 0.0f, 0.0f, 0.0f), u = g;
 #pragma unroll 1
-          for (int q = 0; q < head.cpt; q += 4) {
-            float4 x[4], z[4];
+          for (int q = 0; q < head.cpt; q += kParts) {
+            float4 x[kParts], z[kParts];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < kParts; ++i) {
               x[i] = z[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
               if (q + i < head.cpt) {
                 x[i] = __ldcg(from + (q + i) * part);
@@ -963,7 +1056,7 @@ __global__ void __launch_bounds__(32 * (6 + kFin) + 128 * kWgs, 1)
               }
             }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < kParts; ++i) {
               add4(g, x[i]);
               add4(u, z[i]);
             }
