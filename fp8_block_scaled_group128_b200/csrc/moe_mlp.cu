@@ -33,7 +33,7 @@
 // their chunks and add the parts up in a fixed order, so that the bytes are
 // the same every call:
 //
-//   h   four rows x 128 intermediate columns: SwiGLU, codes and scales
+//   h   one to four rows x 128 intermediate columns: SwiGLU, codes and scales
 //   y   32 output columns of some tokens: the weighted sum over a token's experts
 //
 // Down's chunks follow gate+up's in the list, K-blocks first, then output
@@ -72,9 +72,9 @@ namespace {
 
 constexpr int kPlanThreads = 1024;
 constexpr int kBlockRows = 64;     // tokens of one expert that are walked together
+constexpr int kFin = 2;            // finisher warps (more take registers from the sums)
 constexpr int kBatch = 8;          // units per batch of scale products
 constexpr int kTabs = 4;           // buffers of scale products
-constexpr int kFinRows = 4;        // rows of an h task
 constexpr int64_t kPartFloats = 8 << 20;   // partial sums of a product, but for large problems
 
 constexpr int kSmemBytes = 227 * 1024;
@@ -94,9 +94,10 @@ struct alignas(16) Head {
   int q_gu, cpt;        // units of a gate+up chunk; chunks of a result
   int q_down, cps;      // units of a down chunk; chunks of a block's part of a result
   int n_gu, total;      // chunks of gate+up; of both
-  int groups;           // h tasks of a gate+up result
+  int fin_rows, groups; // rows of an h task; h tasks of a gate+up result
   int n_h, n_tasks;     // h tasks; of both kinds
   int top;              // rows of a token, at most
+  int pad[3];
 };
 
 // What is known before the plan.
@@ -158,7 +159,13 @@ __host__ __device__ inline Head head_of(int blocks, int rows, int most, int top,
   h.cps = down.n;
   h.n_gu = blocks * IB * h.cpt;
   h.total = h.n_gu + blocks * h.cps * KB;
-  h.groups = (most + kFinRows - 1) / kFinRows;
+  // an h task has one row where that is at most three tasks for a finisher warp,
+  // else two or four
+  h.fin_rows = 1;
+  while (h.fin_rows < 4 &&
+         blocks * IB * ((most + h.fin_rows - 1) / h.fin_rows) > 3 * kFin * s.sms)
+    h.fin_rows *= 2;
+  h.groups = (most + h.fin_rows - 1) / h.fin_rows;
   h.n_h = blocks * IB * h.groups;
   h.n_tasks = h.n_h + KB * s.y_tasks;
   h.top = top;
@@ -559,9 +566,8 @@ struct Ring {   // position in a ring of n barriers
   }
 };
 
-// kN: most token columns; kWgs: promotion warpgroups; kFin: finisher warps (2
-// modulo 4, so that the promotion warps begin at a multiple of 4).
-template <int kN, int kWgs, int kFin, bool kE8>
+// kN: most token columns; kWgs: promotion warpgroups.
+template <int kN, int kWgs, bool kE8>
 __global__ void __launch_bounds__(32 * (6 + kFin) + 128 * kWgs, 1)
     moe_mlp_kernel(const __grid_constant__ CUtensorMap tmap_g,
                    const __grid_constant__ CUtensorMap tmap_d,
@@ -653,11 +659,10 @@ __global__ void __launch_bounds__(32 * (6 + kFin) + 128 * kWgs, 1)
   bool all_ready = false;
   auto wait_h = [&](const Chunk& ch) {
     if (all_ready) return true;
-    const bool all = load_acquire(h_done) >= head.n_h;
-    const bool some = load_acquire(args.plan.ready + ch.ready) >= ch.needs;
-    all_ready = __all_sync(0xffffffffu, all);
-    return __all_sync(0xffffffffu, all || some) ||
-           wait_count_warp(args.plan.ready + ch.ready, ch.needs, limit);
+    if (!__all_sync(0xffffffffu, load_acquire(args.plan.ready + ch.ready) >= ch.needs))
+      return wait_count_warp(args.plan.ready + ch.ready, ch.needs, limit);
+    all_ready = __all_sync(0xffffffffu, load_acquire(h_done) >= head.n_h);
+    return true;
   };
 
   if (warp == 0) {
@@ -1022,7 +1027,6 @@ __global__ void __launch_bounds__(32 * (6 + kFin) + 128 * kWgs, 1)
       if (lane == 0) mbar_arrive(&bar.pairs);
     }
     bool pairs_there = false;
-    constexpr int kParts = 8;   // of a result, under way together
     const int64_t gu_row = static_cast<int64_t>(IB) * 256;   // floats of a row of part_gu
     while (!stopped()) {
       int task = 0;
@@ -1034,52 +1038,70 @@ __global__ void __launch_bounds__(32 * (6 + kFin) + 128 * kWgs, 1)
         // lane four of them
         const int s = task / head.groups;
         const int a = s / IB, tile = s - a * IB;
-        const int row0 = act[a].y + (task - s * head.groups) * kFinRows;
-        const int row1 = min(row0 + kFinRows, act[a + 1].y);
+        const int row0 = act[a].y + (task - s * head.groups) * head.fin_rows;
+        const int row1 = min(row0 + head.fin_rows, act[a + 1].y);
         if (row0 < row1) ok = wait_count_warp(args.plan.count_gu + s, head.cpt, limit);
         if (!ok) break;
+        // eight parts are loaded together: of two rows where a row has at most four
+        const bool pair = head.cpt <= 4;
+        const int64_t part = head.rows * gu_row / 4;
 #pragma unroll 1
-        for (int row = row0; row < row1; ++row) {
+        for (int row = row0; row < row1; row += pair ? 2 : 1) {
           const float4* from =
               reinterpret_cast<const float4*>(args.part_gu + row * gu_row + tile * 256) + lane;
-          const int64_t part = head.rows * gu_row / 4;
-          float4 g = make_float4(0.0f, 0.0f, 0.0f, 0.0f), u = g;
+          float4 g[2], u[2];
+          g[0] = u[0] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 1
-          for (int q = 0; q < head.cpt; q += kParts) {
-            float4 x[kParts], z[kParts];
+          for (int q = 0; q < head.cpt; q += 8) {
+            float4 x[8], z[8];
 #pragma unroll
-            for (int i = 0; i < kParts; ++i) {
+            for (int i = 0; i < 8; ++i) {
+              const int r = pair ? i >> 2 : 0, p = pair ? i & 3 : q + i;
               x[i] = z[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-              if (q + i < head.cpt) {
-                x[i] = __ldcg(from + (q + i) * part);
-                z[i] = __ldcg(from + (q + i) * part + 32);
+              if (p < head.cpt && row + r < row1) {
+                x[i] = __ldcg(from + r * (gu_row / 4) + p * part);
+                z[i] = __ldcg(from + r * (gu_row / 4) + p * part + 32);
               }
             }
+            g[1] = x[4];
+            u[1] = z[4];
+            add4(g[0], x[0]);
+            add4(u[0], z[0]);
 #pragma unroll
-            for (int i = 0; i < kParts; ++i) {
-              add4(g, x[i]);
-              add4(u, z[i]);
+            for (int i = 1; i < 4; ++i) {
+              add4(g[0], x[i]);
+              add4(u[0], z[i]);
+              add4(g[1], x[4 + i]);
+              add4(u[1], z[4 + i]);
+            }
+            if (!pair) {
+              add4(g[0], g[1]);
+              add4(u[0], u[1]);
             }
           }
-          const float h[4] = {silu_f32(g.x) * u.x, silu_f32(g.y) * u.y, silu_f32(g.z) * u.z,
-                              silu_f32(g.w) * u.w};
-          // magnitudes are compared as integers, so that a NaN is the largest
-          uint32_t m = 0u;
+#pragma unroll 1
+          for (int r = 0; r < (pair ? 2 : 1) && row + r < row1; ++r) {
+            const float4 gr = r == 0 ? g[0] : g[1], ur = r == 0 ? u[0] : u[1];
+            const float h[4] = {silu_f32(gr.x) * ur.x, silu_f32(gr.y) * ur.y,
+                                silu_f32(gr.z) * ur.z, silu_f32(gr.w) * ur.w};
+            // magnitudes are compared as integers, so that a NaN is the largest
+            uint32_t m = 0u;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) m = max(m, __float_as_uint(h[i]) & 0x7FFFFFFFu);
-          const float amax = __uint_as_float(__reduce_max_sync(0xffffffffu, m));
-          const int64_t at = static_cast<int64_t>(row) * IB + tile;
-          uint32_t q;
-          if constexpr (kE8) {
-            const uint32_t code = ue8m0_code_of_amax(amax);
-            q = codes4f_pow2(h[0], h[1], h[2], h[3], ue8m0_inv_scale(code));
-            if (lane == 0) static_cast<uint8_t*>(args.sh)[at] = static_cast<uint8_t>(code);
-          } else {
-            const float sc = scale_of_amax(amax);
-            q = codes4f(h[0], h[1], h[2], h[3], ScaleDivider(sc));
-            if (lane == 0) static_cast<float*>(args.sh)[at] = sc;
+            for (int i = 0; i < 4; ++i) m = max(m, __float_as_uint(h[i]) & 0x7FFFFFFFu);
+            const float amax = __uint_as_float(__reduce_max_sync(0xffffffffu, m));
+            const int64_t at = static_cast<int64_t>(row + r) * IB + tile;
+            uint32_t q;
+            if constexpr (kE8) {
+              const uint32_t code = ue8m0_code_of_amax(amax);
+              q = codes4f_pow2(h[0], h[1], h[2], h[3], ue8m0_inv_scale(code));
+              if (lane == 0) static_cast<uint8_t*>(args.sh)[at] = static_cast<uint8_t>(code);
+            } else {
+              const float sc = scale_of_amax(amax);
+              q = codes4f(h[0], h[1], h[2], h[3], ScaleDivider(sc));
+              if (lane == 0) static_cast<float*>(args.sh)[at] = sc;
+            }
+            *reinterpret_cast<uint32_t*>(args.qh + at * 128 + lane * 4) = q;
           }
-          *reinterpret_cast<uint32_t*>(args.qh + at * 128 + lane * 4) = q;
         }
         fence_proxy_async_all();   // TMA reads the codes
         __syncwarp();
@@ -1178,10 +1200,10 @@ __global__ void __launch_bounds__(32 * (6 + kFin) + 128 * kWgs, 1)
   }
 }
 
-template <int kN, int kWgs, int kFin, bool kE8>
+template <int kN, int kWgs, bool kE8>
 int launch_mlp(const CUtensorMap (&maps)[4], const MlpArgs& args, int grid, int device,
                cudaStream_t stream) {
-  auto kern = moe_mlp_kernel<kN, kWgs, kFin, kE8>;
+  auto kern = moe_mlp_kernel<kN, kWgs, kE8>;
   static std::once_flag flags[64];
   cudaError_t attr_err = cudaSuccess;
   std::call_once(flags[device], [&] {
@@ -1206,9 +1228,9 @@ int launch_mlp(const CUtensorMap (&maps)[4], const MlpArgs& args, int grid, int 
 template <bool kE8>
 int launch_mlp_n(const CUtensorMap (&maps)[4], const MlpArgs& args, int device,
                  cudaStream_t stream) {
-  if (args.shape.M <= 16) return launch_mlp<16, 2, 2, kE8>(maps, args, args.shape.sms, device, stream);
-  if (args.shape.M <= 32) return launch_mlp<32, 2, 2, kE8>(maps, args, args.shape.sms, device, stream);
-  return launch_mlp<64, 2, 2, kE8>(maps, args, args.shape.sms, device, stream);
+  if (args.shape.M <= 16) return launch_mlp<16, 2, kE8>(maps, args, args.shape.sms, device, stream);
+  if (args.shape.M <= 32) return launch_mlp<32, 2, kE8>(maps, args, args.shape.sms, device, stream);
+  return launch_mlp<64, 2, kE8>(maps, args, args.shape.sms, device, stream);
 }
 
 }  // namespace
