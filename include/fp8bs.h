@@ -375,7 +375,8 @@ int moe_route_topk(const void* logits, int logits_bf16, const float* bias, int s
  *   qw_down [E][K][I], sw_down [E][K/128][I/128].
  *   y_bf16 [M][K], output.
  *   workspace: at least fp8bs_moe_workspace_bytes(M, K, I, E, top_k) bytes, 16-byte
- *       aligned; its contents need no preparation and mean nothing afterwards.
+ *       aligned; its contents need no preparation and mean nothing afterwards. The
+ *       size never falls with M, so that one workspace serves fewer tokens too.
  *       Calls that can run at the same time need workspaces of their own.
  *   0 <= M <= 128, 1 <= E <= 1024, 1 <= top_k <= 32, first_expert >= 0; K and I
  *   positive multiples of 128.

@@ -297,3 +297,20 @@ def test_bounded_wait_reports_timeout_and_recovers(M):
     y = fb.fp8_moe_mlp(*args, workspace=ws)
     assert fb.get_device_error() == 0
     _check(y, args)
+
+
+def test_experts_beyond_32_bit_offsets():
+    """80 experts of 7168 x 2048 (2.3 GB of gate+up codes): the last two as in a
+    call that has only them."""
+    E, K, I = 80, 7168, 2048
+    qa, sa = _rows(3, K, "fp32", 301)
+    two = _experts(2, I, K, "fp32", 302)
+    full = [torch.zeros((E,) + t.shape[1:], dtype=t.dtype, device="cuda") for t in two]
+    for f, t in zip(full, two):
+        f[E - 2:] = t
+    ids = torch.tensor([[E - 1, E - 2], [E - 1, -1], [E - 2, E - 1]], dtype=torch.int32, device="cuda")
+    w = torch.tensor([[0.75, 0.25], [1.0, 0.5], [0.5, 0.5]], device="cuda")
+    y = fb.fp8_moe_mlp(qa, sa, ids, w, *full)
+    part = (qa, sa, ids, w, *two)
+    assert torch.equal(y, fb.fp8_moe_mlp(*part, first_expert=E - 2))
+    _check(y, part, first=E - 2)

@@ -197,3 +197,15 @@ def test_scores_far_from_zero(ng, kg):
 def _check_ids(x, k, **kw):
     ids, _ = fb.moe_route_topk(x, k, **kw)
     np.testing.assert_array_equal(ids.cpu().numpy(), ref.route(x, k, **kw)[0])
+
+
+def test_offsets_beyond_32_bits():
+    """2.25e9 logits: the last rows as in a call of their own."""
+    M, E = 2_200_000, 1024
+    base = _logits(2000, E, seed=13, dtype=torch.bfloat16)
+    x = base.repeat(M // 2000, 1)
+    x[-700:] = _logits(700, E, seed=14, dtype=torch.bfloat16)
+    ids, w = fb.moe_route_topk(x, 4)
+    tail = fb.moe_route_topk(x[-700:], 4)
+    assert torch.equal(ids[-700:], tail[0]) and torch.equal(w[-700:], tail[1])
+    assert torch.equal(ids[:2000], ids[2000:4000])

@@ -247,3 +247,16 @@ def test_many_rows_timeout_is_reported():
     for a, b in zip(fb.fp8_add_rmsnorm_quant(x, residual=res, weight=w), want):
         assert torch.equal(a, b)
     assert fb.get_device_error() == 0
+
+
+def test_offsets_beyond_32_bits():
+    """2.3e9 elements: the last rows as in a call of their own."""
+    M, K, n = 280_000, 8192, 200
+    base, _, w = _inputs(1000, K, seed=22)
+    x = base.repeat(M // 1000, 1)
+    x[-n:] = _inputs(n, K, seed=23)[0]
+    q, s, y, _ = fb.fp8_add_rmsnorm_quant(x, weight=w)
+    tail = fb.fp8_add_rmsnorm_quant(x[-n:], weight=w)
+    for a, b in zip((q, s, y), tail):
+        assert torch.equal(a[-n:], b)
+    assert torch.equal(q[:1000], q[1000:2000])
