@@ -6,7 +6,9 @@ KIND is one of quant_act, quant_weight, prune24, dense_gemm, sparse_gemm,
 ue8m0_gemm, swiglu (N = 2I: the gate+up GEMM with SwiGLU and the next layer's
 quantization, codes only), grouped_gemm and grouped_ue8m0 (M routed token
 rows over 8 experts with the seeded uneven layout, each expert's rows padded
-to 128; N, K per expert).
+to 128; N, K per expert), add_norm (residual, norm and quantization of M rows of
+K), moe_route (M rows of N experts in 8 groups, 8 choices) and moe_mlp (M
+tokens, 2 of 8 experts each, intermediate size N).
 The inputs are the seeded synthetic llama tensors of that shape (deepseek for
 the grouped kinds), prepared on the device by the library's own kernels before
 the ITERS launches of the kernel under test (select those with the profiler's
@@ -95,6 +97,33 @@ def main(argv):
         y = torch.empty(Mp, N, dtype=torch.bfloat16, device=dev)
         fn = lambda: gemm(qa, sa, qw, sw, mid, y=y)  # noqa: E731
         del w, x
+    elif kind == "add_norm":
+        x = synth.activations("llama", M, K, seed=0).to(dev)
+        res = synth.activations("deepseek", M, K, seed=1).to(dev)
+        w = torch.ones(K, dtype=torch.bfloat16, device=dev)
+        q, s, y, r = fb.fp8_add_rmsnorm_quant(x, residual=res, weight=w)
+        fn = lambda: fb.fp8_add_rmsnorm_quant(x, residual=res, weight=w, q=q, s=s, y=y,  # noqa: E731
+                                              residual_out=r)
+    elif kind == "moe_route":
+        g = torch.Generator().manual_seed(0)
+        logits, bias = torch.randn(M, N, generator=g).to(dev), torch.zeros(N, device=dev)
+        ids, wts = fb.moe_route_topk(logits, 8, scoring="sigmoid", bias=bias, n_group=8, topk_group=4)
+        fn = lambda: fb.moe_route_topk(logits, 8, scoring="sigmoid", bias=bias, n_group=8,  # noqa: E731
+                                       topk_group=4, ids=ids, weights=wts)
+    elif kind == "moe_mlp":
+        E = synth.MOE_EXPERTS
+        g = torch.Generator().manual_seed(0)
+        ids = torch.rand(M, E, generator=g).argsort(dim=1)[:, :2].int().to(dev)
+        wts = torch.full((M, 2), 0.5, device=dev)
+        qa, sa = fb.fp8_quant_act_group128(synth.activations("deepseek", M, K, seed=3).to(dev))
+        packed = []
+        for n, k in ((2 * N, K), (K, N)):
+            parts = [fb.fp8_quant_weight_block128(synth.weights("deepseek", n, k, seed=e).to(dev))
+                     for e in range(E)]
+            packed += [torch.stack([q for q, _ in parts]), torch.stack([s for _, s in parts])]
+        ws = torch.empty(fb.moe_workspace_bytes(M, K, N, E, 2), dtype=torch.uint8, device=dev)
+        y = fb.fp8_moe_mlp(qa, sa, ids, wts, *packed, workspace=ws)
+        fn = lambda: fb.fp8_moe_mlp(qa, sa, ids, wts, *packed, y=y, workspace=ws)  # noqa: E731
     else:
         raise SystemExit(f"unknown kind {kind!r}")
     torch.cuda.synchronize()
