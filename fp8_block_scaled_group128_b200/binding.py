@@ -1,4 +1,6 @@
-"""Thin ctypes binding of libfp8bs (the C ABI declared in include/fp8bs.h).
+"""Thin ctypes binding of libfp8bs (the C ABI declared in include/fp8bs.h); the
+calls of the mixture-of-experts block go through a native module of the same C
+calls, _decode.
 
 Argument marshalling only: torch tensors supply device pointers and the
 current CUDA stream; every step of the computation runs in the library's
@@ -7,13 +9,13 @@ fallback: if it is missing, or the device is not a B200, calls raise.
 """
 
 import ctypes
-import functools
 import os
 
 import torch
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libfp8bs.so")
+DECODE_PATH = os.path.join(_HERE, "_decode.so")
 
 FP8BS_OK = 0
 STATUS = {
@@ -364,100 +366,37 @@ def fp8_gemm_swiglu_quant_noalloc(qa, sa, qw_gate_up, sw_gate_up, h, qh, sh, str
     return h, qh, sh
 
 
-# The entry points below take tensors of any one device and any stream of it:
-# the call is made with that device current, and outputs and workspaces that it
-# allocates belong to the launching stream. A decode step makes these calls back
-# to back on little data, so the checks are one expression where nothing is
-# wrong (the reasons are sorted out afterwards) and outputs are shaped after an
-# operand where they can be (1.3 us against 2.3 us for torch.empty, measured).
-
-# handle of the current stream; the public call builds a Stream object first
-# (3.2 us against 0.1 us)
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
-    lambda device: torch.cuda.current_stream(device).cuda_stream)
+# The entry points below take tensors of any one device and any stream of it.
+# Their checks and allocations are native too (csrc/decode_binding.cpp): a decode
+# step makes these calls back to back on little data.
+_decode_module = None
 
 
-def _device_of(t, name):
-    if not (isinstance(t, torch.Tensor) and t.is_cuda):
-        raise TypeError(f"{name} must be a CUDA tensor")
-    return t.get_device()
+def _decode():
+    """The native module (raises if it has not been built)."""
+    global _decode_module
+    if _decode_module is None:
+        if not os.path.exists(DECODE_PATH):
+            raise RuntimeError(
+                f"{DECODE_PATH} is missing: build it with "
+                "`python -m fp8_block_scaled_group128_b200.build`")
+        from . import _decode as native
+        _decode_module = native
+    return _decode_module
 
 
-def _operand(t, dtype, shape, device, name):
-    """Address of a contiguous tensor of the given type, shape and device."""
-    try:
-        if (t.dtype is dtype and t.shape == shape and t.get_device() == device
-                and t.is_contiguous()):
-            return t.data_ptr()
-    except AttributeError:
-        pass
-    _device_of(t, name)
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    raise ValueError(f"{name} is on another device than the first operand")
-
-
-def _matrix(t, name):
-    if t.dim() != 2:
-        raise ValueError(f"{name} must have two dimensions, got {tuple(t.shape)}")
-    return t.shape
-
-
-def _on(device, stream, call, *args):
-    """call(handle of the launching stream, device, *args) with `device` and that
-    stream current."""
+def _call(name, stream, ref, fn, *args):
+    """fn(*args) on `stream` (None: the current one of the operands' device)."""
     if stream is None:
-        if device == torch.cuda.current_device():
-            return call(_raw_stream(device), device, *args)
-        with torch.cuda.device(device):
-            return call(_raw_stream(device), device, *args)
-    if stream.device.index != device:
-        raise ValueError("stream belongs to another device than the operands")
-    with torch.cuda.stream(stream):
-        return call(stream.cuda_stream, device, *args)
-
-
-def _norm_call(handle, dev, name, scale_dtype, x, residual, weight, eps, q, s, y, residual_out,
-               want_y):
-    bf16 = torch.bfloat16
-    M, K = shape = _matrix(x, "x")
-    groups = (M, K // 128)
-    xp = _operand(x, bf16, shape, dev, "x")
-    rp = wp = op = yp = None
-    if weight is not None:
-        wp = _operand(weight, bf16, (K,), dev, "weight")
-    if residual is not None:
-        rp = _operand(residual, bf16, shape, dev, "residual")
-        if residual_out is None:
-            residual_out = torch.empty_like(x)
-            op = residual_out.data_ptr()
-        else:
-            op = _operand(residual_out, bf16, shape, dev, "residual_out")
-    elif residual_out is not None:
-        raise ValueError("residual_out without a residual would be a copy of x")
-    if y is not None:
-        yp = _operand(y, bf16, shape, dev, "y")
-    elif want_y:
-        y = torch.empty_like(x)
-        yp = y.data_ptr()
-    if q is None:
-        q = torch.empty_like(x, dtype=torch.uint8)
-        qp = q.data_ptr()
+        out = fn(*args)
     else:
-        qp = _operand(q, torch.uint8, shape, dev, "q")
-    if s is None:
-        s = x.new_empty(groups, dtype=scale_dtype)
-        sp = s.data_ptr()
-    else:
-        sp = _operand(s, scale_dtype, groups, dev, "s")
-    st = getattr(lib(), name)(xp, rp, wp, eps, M, K, op, yp, qp, sp, handle)
-    if st:
-        raise Fp8bsError(name, st)
-    return q, s, y, residual_out
+        if isinstance(ref, torch.Tensor) and ref.is_cuda and stream.device != ref.device:
+            raise ValueError("stream belongs to another device than the operands")
+        with torch.cuda.stream(stream):
+            out = fn(*args)
+    if out.__class__ is int:
+        raise Fp8bsError(name, out)
+    return out
 
 
 def fp8_add_rmsnorm_quant(x, residual=None, weight=None, eps=1e-6, q=None, s=None, y=None,
@@ -466,46 +405,18 @@ def fp8_add_rmsnorm_quant(x, residual=None, weight=None, eps=1e-6, q=None, s=Non
     returns (q uint8 [M, K], s fp32 [M, K/128], y bf16 [M, K] or None with
     want_y=False, residual_out bf16 [M, K] = x + residual or None without a
     residual). residual_out may be given as `residual` or `x` itself."""
-    return _on(_device_of(x, "x"), stream, _norm_call, "fp8_add_rmsnorm_quant", torch.float32, x,
-               residual, weight, eps, q, s, y, residual_out, want_y)
+    return _call("fp8_add_rmsnorm_quant", stream, x, _decode().norm, False, x, residual, weight, eps,
+                 q, s, y, residual_out, want_y)
 
 
 def fp8_add_rmsnorm_quant_ue8m0(x, residual=None, weight=None, eps=1e-6, q=None, s8=None, y=None,
                                 residual_out=None, want_y=True, stream=None):
     """fp8_add_rmsnorm_quant with UE8M0 scale codes s8 uint8 [M, K/128]."""
-    return _on(_device_of(x, "x"), stream, _norm_call, "fp8_add_rmsnorm_quant_ue8m0", torch.uint8,
-               x, residual, weight, eps, q, s8, y, residual_out, want_y)
+    return _call("fp8_add_rmsnorm_quant_ue8m0", stream, x, _decode().norm, True, x, residual, weight,
+                 eps, q, s8, y, residual_out, want_y)
 
 
 ROUTE_SCORING = {"softmax": 0, "sigmoid": 1}
-
-
-def _route_call(handle, dev, logits, top_k, scoring, bias, n_group, topk_group, renormalize,
-                scale, ids, weights):
-    M, E = shape = _matrix(logits, "logits")
-    dtype = logits.dtype
-    if dtype is not torch.float32 and dtype is not torch.bfloat16:
-        raise TypeError(f"logits must be float32 or bfloat16, got {dtype}")
-    if scoring not in ROUTE_SCORING:
-        raise ValueError(f"scoring must be one of {sorted(ROUTE_SCORING)}, got {scoring!r}")
-    lp = _operand(logits, dtype, shape, dev, "logits")
-    bp = None if bias is None else _operand(bias, torch.float32, (E,), dev, "bias")
-    out = (M, max(top_k, 0))
-    if ids is None:
-        ids = logits.new_empty(out, dtype=torch.int32)
-        ip = ids.data_ptr()
-    else:
-        ip = _operand(ids, torch.int32, out, dev, "ids")
-    if weights is None:
-        weights = torch.empty_like(ids, dtype=torch.float32)
-        wp = weights.data_ptr()
-    else:
-        wp = _operand(weights, torch.float32, out, dev, "weights")
-    st = lib().moe_route_topk(lp, dtype is torch.bfloat16, bp, ROUTE_SCORING[scoring], M, E, top_k,
-                              n_group, topk_group, bool(renormalize), scale, ip, wp, handle)
-    if st:
-        raise Fp8bsError("moe_route_topk", st)
-    return ids, weights
 
 
 def moe_route_topk(logits, top_k, scoring="softmax", bias=None, n_group=1, topk_group=1,
@@ -513,50 +424,14 @@ def moe_route_topk(logits, top_k, scoring="softmax", bias=None, n_group=1, topk_
     """The top_k experts of every row of logits [M, E] (fp32 or bf16) and their
     weights: (ids int32 [M, top_k], weights fp32 [M, top_k]), best first. bias
     (fp32 [E]) and groups (n_group > 1) need scoring="sigmoid"."""
-    return _on(_device_of(logits, "logits"), stream, _route_call, logits, top_k, scoring, bias,
-               n_group, topk_group, renormalize, scale, ids, weights)
+    if scoring not in ROUTE_SCORING:
+        raise ValueError(f"scoring must be one of {sorted(ROUTE_SCORING)}, got {scoring!r}")
+    return _call("moe_route_topk", stream, logits, _decode().route, logits, top_k,
+                 ROUTE_SCORING[scoring], bias, n_group, topk_group, renormalize, scale, ids, weights)
 
 
-@functools.lru_cache(maxsize=4096)
 def moe_workspace_bytes(M, K, I, E, top_k):
     return int(lib().fp8bs_moe_workspace_bytes(M, K, I, E, top_k))
-
-
-def _moe_call(handle, dev, name, scale_dtype, qa, sa, ids, weights, qg, sg, qd, sd, first_expert, y,
-              workspace):
-    u8, f32 = torch.uint8, torch.float32
-    M, K = _matrix(qa, "qa")
-    top_k = _matrix(ids, "ids")[1]
-    pairs = (M, top_k)
-    if qd.dim() != 3:
-        raise ValueError(f"qw_down must have three dimensions, got {tuple(qd.shape)}")
-    E, _, I = qd.shape
-    KB, IB = K // 128, I // 128
-    args = (_operand(qa, u8, (M, K), dev, "qa"),
-            _operand(sa, scale_dtype, (M, KB), dev, "sa"),
-            _operand(ids, torch.int32, pairs, dev, "ids"),
-            _operand(weights, f32, pairs, dev, "weights"),
-            _operand(qg, u8, (E, 2 * I, K), dev, "qw_gate_up"),
-            _operand(sg, scale_dtype, (E, 2 * IB, KB), dev, "sw_gate_up"),
-            _operand(qd, u8, (E, K, I), dev, "qw_down"),
-            _operand(sd, scale_dtype, (E, KB, IB), dev, "sw_down"))
-    if y is None:
-        y = torch.empty_like(qa, dtype=torch.bfloat16)
-        yp = y.data_ptr()
-    else:
-        yp = _operand(y, torch.bfloat16, (M, K), dev, "y")
-    if workspace is None:
-        size = moe_workspace_bytes(M, K, I, E, top_k)
-        workspace = qa.new_empty(size)
-    else:
-        if _device_of(workspace, "workspace") != dev or not workspace.is_contiguous():
-            raise ValueError("workspace must be a contiguous tensor on the operands' device")
-        size = workspace.numel() * workspace.element_size()
-    st = getattr(lib(), name)(*args, yp, M, K, I, E, top_k, first_expert, workspace.data_ptr(), size,
-                              handle)
-    if st:
-        raise Fp8bsError(name, st)
-    return y
 
 
 def fp8_moe_mlp(qa, sa, ids, weights, qw_gate_up, sw_gate_up, qw_down, sw_down, first_expert=0,
@@ -567,15 +442,15 @@ def fp8_moe_mlp(qa, sa, ids, weights, qw_gate_up, sw_gate_up, qw_down, sw_down, 
     outside [first_expert, first_expert + E) add nothing. A workspace
     (moe_workspace_bytes) can be kept by the caller; calls that may overlap need
     one each."""
-    return _on(_device_of(qa, "qa"), stream, _moe_call, "fp8_moe_mlp", torch.float32, qa, sa, ids,
-               weights, qw_gate_up, sw_gate_up, qw_down, sw_down, first_expert, y, workspace)
+    return _call("fp8_moe_mlp", stream, qa, _decode().mlp, False, qa, sa, ids, weights, qw_gate_up,
+                 sw_gate_up, qw_down, sw_down, first_expert, y, workspace)
 
 
 def fp8_moe_mlp_ue8m0(qa, sa8, ids, weights, qw_gate_up, sw8_gate_up, qw_down, sw8_down,
                       first_expert=0, y=None, workspace=None, stream=None):
     """fp8_moe_mlp with UE8M0 scale codes throughout."""
-    return _on(_device_of(qa, "qa"), stream, _moe_call, "fp8_moe_mlp_ue8m0", torch.uint8, qa, sa8,
-               ids, weights, qw_gate_up, sw8_gate_up, qw_down, sw8_down, first_expert, y, workspace)
+    return _call("fp8_moe_mlp_ue8m0", stream, qa, _decode().mlp, True, qa, sa8, ids, weights,
+                 qw_gate_up, sw8_gate_up, qw_down, sw8_down, first_expert, y, workspace)
 
 
 def fp8_gather_columns(src, dst=None, stream=None):

@@ -86,3 +86,59 @@ def test_block_in_a_graph():
     want, tol = ref.moe(got[0], got[1], got[5], got[6], *args[5])
     assert bool(((got[7].double() - want).abs() <= tol).all())
     assert not torch.equal(got[7], first[7])
+
+
+def test_calls_keep_nothing():
+    """Outputs die with their last reference, also those of refused calls; given
+    outputs are returned as they are."""
+    import gc
+    import sys
+    x, res, wn, wr, bias, experts = _inputs(4, 512, 256, 8, "fp32", seed=9)
+    logits = torch.randn(4, 8, device="cuda")
+    q, s = fb.fp8_add_rmsnorm_quant(x, residual=res, weight=wn)[:2]
+    ids, w = fb.moe_route_topk(logits, 2)
+    y = fb.fp8_moe_mlp(q, s, ids, w, *experts)
+    again = fb.fp8_add_rmsnorm_quant(x, residual=res, weight=wn, q=q, s=s)
+    assert again[0] is q and again[1] is s
+    assert fb.moe_route_topk(logits, 2, ids=ids, weights=w)[0] is ids
+    assert fb.fp8_moe_mlp(q, s, ids, w, *experts, y=y) is y
+    del again
+    torch.cuda.synchronize()
+    gc.collect()
+    used, refs = torch.cuda.memory_allocated(), [sys.getrefcount(t) for t in (x, q, ids, y)]
+    for _ in range(50):
+        fb.fp8_add_rmsnorm_quant(x, residual=res, weight=wn, q=q)
+        fb.moe_route_topk(logits, 2, ids=ids)
+        fb.fp8_moe_mlp(q, s, ids, w, *experts)
+        fb.fp8_moe_mlp(q, s, ids, w, *experts, y=y)
+        for bad in (lambda: fb.fp8_add_rmsnorm_quant(x, residual=res, eps=-1.0, q=q),
+                    lambda: fb.moe_route_topk(logits, 9, ids=None),
+                    lambda: fb.fp8_moe_mlp(q, s, ids, w, *experts, first_expert=-1, y=y)):
+            with pytest.raises(fb.Fp8bsError):
+                bad()
+        with pytest.raises(TypeError):
+            fb.moe_route_topk(logits, "2")
+        with pytest.raises(TypeError):
+            fb.fp8_add_rmsnorm_quant(x, residual=res, eps="small")
+        with pytest.raises(ValueError):
+            fb.fp8_add_rmsnorm_quant(x, residual=res, q=q, s=s[:2])
+    torch.cuda.synchronize()
+    assert torch.cuda.memory_allocated() == used
+    assert [sys.getrefcount(t) for t in (x, q, ids, y)] == refs
+
+
+def test_a_stream_of_the_callers_choice():
+    """The current stream, and one that is given: outputs belong to it."""
+    x, res, wn, wr, bias, experts = _inputs(16, 512, 256, 8, "fp32", seed=10)
+    want = _block(x, res, wn, wr, bias[:8].contiguous(), experts, "fp32")
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    q, s, h, r = fb.fp8_add_rmsnorm_quant(x, residual=res, weight=wn, stream=side)
+    with torch.cuda.stream(side):
+        logits = (h @ wr.t()).float()
+        ids, w = fb.moe_route_topk(logits, 4, scoring="sigmoid", bias=bias, n_group=4, topk_group=2,
+                                   scale=2.5)
+    y = fb.fp8_moe_mlp(q, s, ids, w, *experts, stream=side)
+    side.synchronize()
+    for a, b in zip((q, s, h, r, ids, w, y), [want[i] for i in (0, 1, 2, 3, 5, 6, 7)]):
+        assert torch.equal(a, b)
