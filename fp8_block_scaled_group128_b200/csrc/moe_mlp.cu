@@ -1043,8 +1043,8 @@ __global__ void __launch_bounds__(32 * (6 + kFin) + 128 * kWgs, 1)
       task = __shfl_sync(0xffffffffu, task, 0);
       if (task >= head.n_tasks) break;
       if (task < head.n_h) {
-        // h = silu(g) * u of up to 8 rows: the warp has a row's 128 columns, a
-        // lane four of them
+        // h = silu(g) * u of some rows: the warp has a row's 128 columns, a lane
+        // four of them
         const int s = task / head.groups;
         const int a = s / IB, tile = s - a * IB;
         const int row0 = act[a].y + (task - s * head.groups) * head.fin_rows;
@@ -1149,22 +1149,17 @@ __global__ void __launch_bounds__(32 * (6 + kFin) + 128 * kWgs, 1)
             for (int i = 0; i < 4; ++i) {
               const int slot = 4 * i + grp;
               const int item = it + (slot >> lg), p = p0 + (slot & ((1 << lg) - 1));
+              const int j = head.cps == 1 ? p : p / head.cps;
+              const bool there = item < item1 && p < parts;
+              const int pair = there ? (item >> 2) * args.shape.top_k + j : 0;
+              const int r = there ? pair_row[pair] : -1;
+              w[i] = r >= 0 ? pair_w[pair] : 0.0f;
+              const float* from = args.part_down +
+                                  (static_cast<int64_t>(p - j * head.cps) * head.rows + r) *
+                                      args.shape.K +
+                                  tile * 128 + (item & 3) * 32;
               x[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-              w[i] = 0.0f;
-              if (item < item1 && p < parts) {
-                const int j = p / head.cps;
-                const int pair = (item >> 2) * args.shape.top_k + j;
-                const int r = pair_row[pair];
-                if (r >= 0) {
-                  w[i] = pair_w[pair];
-                  x[i] = __ldcg(reinterpret_cast<const float4*>(
-                                    args.part_down +
-                                    (static_cast<int64_t>(p - j * head.cps) * head.rows + r) *
-                                        args.shape.K +
-                                    tile * 128 + (item & 3) * 32) +
-                                (lane & 7));
-                }
-              }
+              if (r >= 0) x[i] = __ldcg(reinterpret_cast<const float4*>(from) + (lane & 7));
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
