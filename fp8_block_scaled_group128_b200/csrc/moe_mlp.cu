@@ -385,7 +385,7 @@ __device__ __forceinline__ void plan_few(const int32_t* ids, const float* weight
 // The order of an expert's rows comes from atomics here and may differ from
 // call to call; nothing computed depends on it. The block has a thread for every
 // expert at least, and two warps at least.
-__global__ void __launch_bounds__(kPlanThreads)
+__global__ void __launch_bounds__(kPlanThreads, 1)
     moe_plan_kernel(const int32_t* __restrict__ ids, const float* __restrict__ weights, int pairs,
                     int E, int first_expert, const Plan plan, const Shape shape) {
   __shared__ int expert[kMoeMaxM * kMoeMaxTopK];   // local expert of a choice, -1: none

@@ -373,7 +373,7 @@ int moe_route_topk(const void* logits, int logits_bf16, const float* bias, int s
  *       gets zeros. A token may name an expert more than once: the weights add.
  *   qw_gate_up [E][2I][K], sw_gate_up [E][2I/128][K/128] ([W_gate; W_up]);
  *   qw_down [E][K][I], sw_down [E][K/128][I/128].
- *   y_bf16 [M][K], output.
+ *   y_bf16 [M][K], output; it and the workspace overlap no operand.
  *   workspace: at least fp8bs_moe_workspace_bytes(M, K, I, E, top_k) bytes, 16-byte
  *       aligned; its contents need no preparation and mean nothing afterwards. The
  *       size never falls with M, so that one workspace serves fewer tokens too.

@@ -314,3 +314,24 @@ def test_experts_beyond_32_bit_offsets():
     part = (qa, sa, ids, w, *two)
     assert torch.equal(y, fb.fp8_moe_mlp(*part, first_expert=E - 2))
     _check(y, part, first=E - 2)
+
+
+@pytest.mark.parametrize("M,E,k", [(4, 5, 4), (1, 40, 32), (8, 3, 4), (31, 6, 1), (2, 200, 16), (16, 2, 2)])
+def test_few_choices(M, E, k):
+    """At most 32 choices: repeated experts, ids outside the range, whole rows
+    without an expert, in one call."""
+    g = torch.Generator().manual_seed(400 + M)
+    args = list(_case(M, 384, 256, E, 1, "fp32", seed=90 + M))
+    ids = torch.randint(-1, E + 2, (M, k), generator=g).to(torch.int32)
+    if M > 2:
+        ids[1] = -1
+        ids[2] = E - 1
+    args[2], args[3] = ids.cuda(), torch.randn(M, k, generator=g).cuda()
+    y = fb.fp8_moe_mlp(*args)
+    _check(y, args)
+    # more of the same tokens: the plan for many choices
+    more = [torch.cat([a] * (33 // (M * k) + 1)) for a in args[:4]] + args[4:]
+    assert more[2].numel() > 32
+    _check(fb.fp8_moe_mlp(*more), more)
+    args[2] = torch.full_like(args[2], E)
+    assert bool((fb.fp8_moe_mlp(*args) == 0).all())
