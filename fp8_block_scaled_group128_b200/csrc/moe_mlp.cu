@@ -512,10 +512,12 @@ struct MlpArgs {
   int* err;
 };
 
+// A UE8M0 code c stands for 2^(c - 127), and 255 for NaN.
 __device__ __forceinline__ float scale_value(const void* s, int64_t i, bool e8) {
   if (!e8) return __ldcg(static_cast<const float*>(s) + i);
   const uint32_t c = __ldcg(static_cast<const uint8_t*>(s) + i);
-  return c == 0u ? __uint_as_float(0x00400000u) : __uint_as_float(c << 23);
+  const uint32_t odd = c == 0u ? 0x00400000u : 0x7FFFFFFFu;
+  return __uint_as_float(c - 1u < 254u ? c << 23 : odd);
 }
 
 __device__ __forceinline__ int load_acquire(const int* p) {

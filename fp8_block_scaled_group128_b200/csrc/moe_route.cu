@@ -65,10 +65,10 @@ __device__ __forceinline__ uint64_t warp_max(uint64_t k) {
 __device__ __forceinline__ float sigmoid32(float x) { return 1.0f / (1.0f + expf(-x)); }
 
 // sigmoid(x) in double precision for -60 <= x <= 60 without a branch, so that
-// the experts of a lane overlap (above 60 it is 1 to 2^-86): e^-x = 2^n e^r with r = -x - n ln 2 (ln 2 in two
-// parts, Cody and Waite), e^r by its Taylor series to r^13 (|r| <= ln 2 / 2:
-// the rest is below 2^-57), and 1 / (1 + e^-x) by two Newton steps from an fp32
-// reciprocal.
+// the experts of a lane overlap (above 60 it is 1 to 2^-86): e^-x = 2^n e^r with
+// r = -x - n ln 2 (ln 2 in two parts, Cody and Waite), e^r by its Taylor series
+// to r^13 (|r| <= ln 2 / 2: the rest is below 2^-57), and 1 / (1 + e^-x) by two
+// Newton steps from an fp32 reciprocal.
 __device__ __forceinline__ double sigmoid64(double x) {
   const double magic = 6755399441055744.0;             // 1.5 * 2^52: rounds to an integer
   const double t = fma(-x, 1.4426950408889634, magic);

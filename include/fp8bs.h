@@ -380,7 +380,8 @@ int moe_route_topk(const void* logits, int logits_bf16, const float* bias, int s
  *       Calls that can run at the same time need workspaces of their own.
  *   0 <= M <= 128, 1 <= E <= 1024, 1 <= top_k <= 32, first_expert >= 0; K and I
  *   positive multiples of 128.
- * The _ue8m0 form takes all scales as UE8M0 codes and quantizes h with them.
+ * The _ue8m0 form takes all scales as UE8M0 codes (255: NaN) and quantizes h with
+ * them.
  * Results are deterministic: the same inputs give the same bytes every call.
  */
 int fp8_moe_mlp(const void* qa, const float* sa, const int32_t* ids, const float* weights,

@@ -178,6 +178,29 @@ def test_zero_token_and_nan_token():
     _check(y[keep], part)
 
 
+def test_ue8m0_nan_scales():
+    """Code 255 is NaN: of a token, of gate+up, of down; the other results stay."""
+    args = list(_case(18, 256, 256, 4, 2, "ue8m0", seed=81))
+    clean = fb.fp8_moe_mlp_ue8m0(*args)
+    ids = args[2]
+    sa, sg, sd = args[1].clone(), args[5].clone(), args[7].clone()
+    sa[9, 1] = 255
+    y = fb.fp8_moe_mlp_ue8m0(args[0], sa, *args[2:])
+    keep = torch.arange(18, device="cuda") != 9
+    assert bool(y[9].isnan().all()) and torch.equal(y[keep], clean[keep])
+    hit = (ids == 2).any(dim=1)
+    assert bool(hit.any()) and not bool(hit.all())
+    for block in (1, 3):   # gate rows 128 to 255, up rows 128 to 255
+        s = sg.clone()
+        s[2, block, 0] = 255
+        y = fb.fp8_moe_mlp_ue8m0(*args[:5], s, *args[6:])
+        assert bool(y[hit].isnan().all()) and torch.equal(y[~hit], clean[~hit])
+    sd[2, 1, 1] = 255      # output columns 128 to 255
+    y = fb.fp8_moe_mlp_ue8m0(*args[:7], sd)
+    assert bool(y[hit][:, 128:].isnan().all()) and torch.equal(y[~hit], clean[~hit])
+    assert torch.equal(y[:, :128], clean[:, :128])
+
+
 def test_deterministic_and_batch_rows_agree():
     args = _case(64, 1024, 512, 8, 2, "fp32", seed=73)
     y = fb.fp8_moe_mlp(*args)
