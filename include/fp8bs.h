@@ -382,6 +382,7 @@ int moe_route_topk(const void* logits, int logits_bf16, const float* bias, int s
  *   positive multiples of 128.
  * The _ue8m0 form takes all scales as UE8M0 codes (255: NaN) and quantizes h with
  * them.
+ * A row whose h is not finite somewhere (NaN, or beyond fp32) gives NaN.
  * Results are deterministic: the same inputs give the same bytes every call.
  */
 int fp8_moe_mlp(const void* qa, const float* sa, const int32_t* ids, const float* weights,

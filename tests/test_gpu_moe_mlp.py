@@ -201,6 +201,24 @@ def test_ue8m0_nan_scales():
     assert torch.equal(y[:, :128], clean[:, :128])
 
 
+@pytest.mark.parametrize("fmt", FMT)
+def test_h_beyond_fp32(fmt):
+    """h of one token overflows: its row is NaN, the others stay."""
+    args = list(_case(18, 256, 256, 4, 2, fmt, seed=83))
+    run = fb.fp8_moe_mlp if fmt == "fp32" else fb.fp8_moe_mlp_ue8m0
+    clean = run(*args)
+    args[1] = args[1].clone()
+    args[1][5] = 2.0 ** 70 if fmt == "fp32" else 197
+    a = ref.dequant_rows(args[0][5:6], args[1][5:6])
+    w = ref.dequant_blocks(args[4], args[5])[int(args[2][5, 0])]
+    g, u = (a @ w.T).chunk(2, dim=-1)
+    assert float((g.clamp(min=0) * u).abs().max()) > 1e40
+    y = run(*args)
+    assert bool(y[5].isnan().all())
+    keep = torch.arange(18, device="cuda") != 5
+    assert torch.equal(y[keep], clean[keep])
+
+
 def test_deterministic_and_batch_rows_agree():
     args = _case(64, 1024, 512, 8, 2, "fp32", seed=73)
     y = fb.fp8_moe_mlp(*args)
