@@ -252,8 +252,8 @@ __global__ void __launch_bounds__(kRowThreads) norm_row_kernel(const RowArgs a) 
       r = make_uint4(hadd_bf16x2(r.x, b.x), hadd_bf16x2(r.y, b.y), hadd_bf16x2(r.z, b.z),
                      hadd_bf16x2(r.w, b.w));
       row[c] = r;
-      if (a.n.res_out != nullptr) a.n.res_out[base + c] = r;
     }
+    if (a.n.res_out != nullptr) a.n.res_out[base + c] = r;
     float f[8];
     unpack8(r, f);
 #pragma unroll

@@ -1,0 +1,62 @@
+"""fp8_add_rmsnorm_quant (and its UE8M0 form): calls of the C entry points that
+the Python binding does not make."""
+
+import ctypes
+
+import pytest
+import torch
+
+from fp8_block_scaled_group128_b200 import binding as fb
+from fp8_block_scaled_group128_b200 import synth
+
+import moe_ref as ref
+from gpu_util import require_gpu, to_dev
+
+pytestmark = pytest.mark.gpu
+FMT = ["fp32", "ue8m0"]
+EPS = 1e-6
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    require_gpu()
+    yield
+    assert fb.get_device_error() == 0
+
+
+def _fn(fmt):
+    return fb.fp8_add_rmsnorm_quant if fmt == "fp32" else fb.fp8_add_rmsnorm_quant_ue8m0
+
+
+def _inputs(M, K, seed):
+    x = to_dev(synth.activations("llama", M, K, seed=seed))
+    res = to_dev(synth.activations("deepseek", M, K, seed=seed + 1))
+    w = to_dev(synth.uniform_bf16((K,), 0.25, 2.0, seed=seed))
+    return x, res, w
+
+
+@pytest.mark.parametrize("fmt", FMT)
+@pytest.mark.parametrize("K", [384, 4096])
+@pytest.mark.parametrize("M", [5, 148, 149, 1037])
+def test_residual_out_without_a_residual(M, K, fmt):
+    """Through the C ABI: with a NULL residual, residual_out is a copy of x (or
+    x itself), whatever the number of rows; the other outputs stay."""
+    x, _, w = _inputs(M, K, seed=M + K)
+    want = _fn(fmt)(x, weight=w, eps=EPS)
+    call = getattr(fb.lib(), _fn(fmt).__name__)
+
+    def run(xp, out):
+        q, s, y = (torch.zeros_like(t) for t in want[:3])
+        args = [ctypes.c_void_p(t if t is None else t.data_ptr()) for t in (xp, None, w, out, y, q, s)]
+        status = call(*args[:3], EPS, M, K, *args[3:],
+                      ctypes.c_void_p(torch.cuda.current_stream().cuda_stream))
+        assert status == 0
+        for a, b in zip((q, s, y), want):
+            assert torch.equal(a, b)
+
+    out = torch.full((M + 1, K), 5.0, dtype=torch.bfloat16, device="cuda")
+    run(x, out)
+    assert torch.equal(out[:M], x) and bool((out[M] == 5).all())
+    same = x.clone()
+    run(same, same)
+    assert torch.equal(same, x)
