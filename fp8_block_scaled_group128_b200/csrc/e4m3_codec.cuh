@@ -213,7 +213,14 @@ __device__ __forceinline__ uint32_t ue8m0_code_of_amax(float amax) {
   return eb == 0 ? 0u : static_cast<uint32_t>(min(max(code, 0), 254));
 }
 
-// 1 / s = 2^(127 - c) as an fp32 value (normal for c <= 253; 2^-127 for 254).
+// The code for values of fp32: an infinite or NaN amax gives 255 (NaN), as it
+// gives an fp32 scale of NaN.
+__device__ __forceinline__ uint32_t ue8m0_code_or_nan(float amax) {
+  return amax <= 3.402823466e38f ? ue8m0_code_of_amax(amax) : 255u;
+}
+
+// 1 / s = 2^(127 - c) as an fp32 value (normal for c <= 253; 2^-127 for 254
+// and 255).
 __device__ __forceinline__ float ue8m0_inv_scale(uint32_t code) {
   return code >= 254u ? __uint_as_float(0x00400000u) : __uint_as_float((254u - code) << 23);
 }

@@ -1103,8 +1103,7 @@ __global__ void __launch_bounds__(32 * (6 + kFin) + 128 * kWgs, 1)
             const int64_t at = static_cast<int64_t>(row + r) * IB + tile;
             uint32_t q;
             if constexpr (kE8) {
-              // (an infinite or NaN h makes the group NaN, as an fp32 scale does)
-              const uint32_t code = amax <= 3.402823466e38f ? ue8m0_code_of_amax(amax) : 255u;
+              const uint32_t code = ue8m0_code_or_nan(amax);
               q = codes4f_pow2(h[0], h[1], h[2], h[3], ue8m0_inv_scale(code));
               if (lane == 0) static_cast<uint8_t*>(args.sh)[at] = static_cast<uint8_t>(code);
             } else {

@@ -166,7 +166,7 @@ __global__ void __launch_bounds__(1024) norm_quant_kernel(const NormArgs a) {
     const float amax = __uint_as_float(mx);
     uint2 q;
     if constexpr (kE8) {
-      const uint32_t code = ue8m0_code_of_amax(amax);
+      const uint32_t code = ue8m0_code_or_nan(amax);
       q = encode8f_pow2(n, ue8m0_inv_scale(code));
       if (on && (t & 15) == 0)
         static_cast<uint8_t*>(a.s)[(base + c) >> 4] = static_cast<uint8_t>(code);
@@ -298,7 +298,7 @@ __global__ void __launch_bounds__(kRowThreads) norm_row_kernel(const RowArgs a) 
       mx = absmax_nan(mx, __shfl_xor_sync(0xffffffffu, mx, off));
     uint2 q;
     if constexpr (kE8) {
-      const uint32_t code = ue8m0_code_of_amax(mx);
+      const uint32_t code = ue8m0_code_or_nan(mx);
       q = encode8f_pow2(n, ue8m0_inv_scale(code));
       if (on && (t & 15) == 0)
         static_cast<uint8_t*>(a.n.s)[(base + c) >> 4] = static_cast<uint8_t>(code);

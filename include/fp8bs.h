@@ -310,8 +310,9 @@ int fp8_gather_columns(const void* src_bf16, int64_t P, int64_t M, int64_t Np, v
  * except where n / s lies within two fp32 ulps of the middle between two codes.
  * M >= 149 takes another kernel than fewer rows: the same row can differ in such
  * a code, and in the last bits of n, between the two.
- * K a positive multiple of 128, at most 65536. A row with a NaN, or an infinity,
- * gives NaN in the groups where n is NaN.
+ * K a positive multiple of 128, at most 65536. A group with an n that is NaN or
+ * beyond fp32 gets the scale NaN (UE8M0: code 255). A row with a NaN is NaN
+ * throughout; in one with an infinity n is NaN there and 0 elsewhere.
  */
 int fp8_add_rmsnorm_quant(const void* x_bf16, const void* residual_bf16, const void* weight_bf16,
                           float eps, int64_t M, int64_t K, void* residual_out_bf16, void* y_bf16,

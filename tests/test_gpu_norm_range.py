@@ -60,3 +60,30 @@ def test_residual_out_without_a_residual(M, K, fmt):
     same = x.clone()
     run(same, same)
     assert torch.equal(same, x)
+
+
+@pytest.mark.parametrize("fmt", FMT)
+@pytest.mark.parametrize("M", [6, 200])
+def test_norm_beyond_fp32(M, fmt):
+    """n beyond fp32 in one place, and a NaN weight in another: those groups'
+    scales are NaN in both forms, y is infinite or NaN there, and the other
+    groups and the rows without such an n stay."""
+    x, res, w = _inputs(M, 640, seed=31)
+    w[200], w[630] = 3.0e38, float("nan")
+    x[:, 200] = 4 * (x.abs() + res.abs()).amax(dim=1)
+    res[:, 200] = 0
+    x[1, 200] = 0
+    n = ref.norm_rows(x, res, w, EPS)[0]
+    big = torch.arange(M, device="cuda") != 1
+    assert bool((n[big, 200] > 4e38).all()) and float(n[1, 200]) == 0
+    q, s, y, _ = _fn(fmt)(x, residual=res, weight=w, eps=EPS)
+    nan = s.isnan() if fmt == "fp32" else s == 255
+    hit = torch.zeros(M, 5, dtype=torch.bool, device="cuda")
+    hit[:, 4] = True
+    hit[big, 1] = True
+    assert torch.equal(nan, hit)
+    assert bool(y[big, 200].isinf().all()) and bool(y[:, 630].isnan().all())
+    for rows, groups in ((big, [0, 2, 3]), (~big, [0, 1, 2, 3])):
+        cols = torch.cat([torch.arange(128 * g, 128 * g + 128) for g in groups]).cuda()
+        ref.check_norm(n[rows][:, cols], fmt, q[rows][:, cols].contiguous(),
+                       s[rows][:, groups], y[rows][:, cols])
