@@ -305,7 +305,8 @@ int fp8_gather_columns(const void* src_bf16, int64_t P, int64_t M, int64_t Np, v
  *       overlap.
  *   y_bf16 [M][K] or NULL (the router of a mixture of experts reads it).
  *   q_e4m3 [M][K], s [M][K/128] fp32 (the _ue8m0 form: codes, one byte each).
- *   eps >= 0 and finite.
+ *   eps >= 0 and finite. Finite rows may be of any size: squares beyond fp32 are
+ *       no less exact. With eps = 0 a row of zeros gives NaN (0 / 0).
  * The codes come from the fp32 n (not from y). They are those of e4m3(n / s)
  * except where n / s lies within two fp32 ulps of the middle between two codes.
  * M >= 149 takes another kernel than fewer rows: the same row can differ in such

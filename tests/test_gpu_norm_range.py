@@ -1,5 +1,5 @@
 """fp8_add_rmsnorm_quant (and its UE8M0 form): calls of the C entry points that
-the Python binding does not make."""
+the Python binding does not make, and values at the ends of fp32's range."""
 
 import ctypes
 
@@ -87,3 +87,49 @@ def test_norm_beyond_fp32(M, fmt):
         cols = torch.cat([torch.arange(128 * g, 128 * g + 128) for g in groups]).cuda()
         ref.check_norm(n[rows][:, cols], fmt, q[rows][:, cols].contiguous(),
                        s[rows][:, groups], y[rows][:, cols])
+
+
+def _scaled_rows(copies, K, powers, seed):
+    """Rows of both signs up to 2^p, for every p `copies` times, neighbours of
+    different p; the first two elements are 2^p and (the smallest bf16) 2^-133."""
+    g = torch.Generator().manual_seed(seed)
+    v = torch.rand(copies, len(powers), K, generator=g, dtype=torch.float64) * 2 - 1
+    v[..., 0] = 1.0
+    v *= torch.exp2(torch.tensor(powers, dtype=torch.float64))[None, :, None]
+    v[..., 1] = 2.0 ** -133
+    return v.view(-1, K).to(torch.bfloat16).cuda()
+
+
+@pytest.mark.parametrize("fmt", FMT)
+@pytest.mark.parametrize("eps,powers", [
+    (0.0, (-133, -130, -126, -100, -76, -66, -50, 0, 50, 63, 64, 76, 100, 120, 126, 127, 127.99)),
+    (2.0 ** -149, (-70, -50, 0, 64, 127)), (1e-6, (-80, -50, 0, 62, 65, 110, 127)),
+    (1e20, (-20, 20, 60, 64, 127)), (3e38, (0, 50, 64, 120, 127))])
+@pytest.mark.parametrize("copies,K", [(1, 128), (60, 128), (60, 384), (1, 1152), (60, 1152),
+                                      (35, 4096), (1, 14336), (35, 14336), (1, 65536)])
+def test_squares_beyond_fp32(copies, K, eps, powers, fmt):
+    """Finite rows whose squares, or their sum, lie outside the range of fp32,
+    next to ordinary ones: the norm is that of the formula."""
+    x = _scaled_rows(copies, K, powers, seed=K + copies)
+    w = to_dev(synth.uniform_bf16((K,), 0.25, 2.0, seed=K))
+    n = ref.norm_rows(x, None, w, eps)[0]
+    assert bool(n.isfinite().all()) and bool((n.abs().amax(dim=1) > 0).all())
+    q, s, y, _ = _fn(fmt)(x, weight=w, eps=eps)
+    ref.check_norm(n, fmt, q, s, y)
+    # (x + res is exact here: r = x / 2)
+    res = torch.where(x.abs() >= 2.0 ** -120, x * -0.5, torch.zeros_like(x))
+    n, r_ref = ref.norm_rows(x, res, w, eps)
+    q, s, y, r = _fn(fmt)(x, residual=res, weight=w, eps=eps)
+    assert torch.equal(r, r_ref)
+    ref.check_norm(n, fmt, q, s, y)
+
+
+@pytest.mark.parametrize("M", [3, 301])
+def test_zero_row_without_eps(M):
+    """0 / sqrt(0): NaN, as the formula has it, in that row only."""
+    x, _, w = _inputs(M, 768, seed=33)
+    x[1] = 0
+    q, s, y, _ = fb.fp8_add_rmsnorm_quant(x, weight=w, eps=0.0)
+    assert bool(y[1].isnan().all()) and bool(s[1].isnan().all())
+    keep = torch.arange(M, device="cuda") != 1
+    ref.check_norm(ref.norm_rows(x, None, w, 0.0)[0][keep], "fp32", q[keep], s[keep], y[keep])
