@@ -133,3 +133,32 @@ def test_zero_row_without_eps(M):
     assert bool(y[1].isnan().all()) and bool(s[1].isnan().all())
     keep = torch.arange(M, device="cuda") != 1
     ref.check_norm(ref.norm_rows(x, None, w, 0.0)[0][keep], "fp32", q[keep], s[keep], y[keep])
+
+
+@pytest.mark.parametrize("M", [148, 20_000])
+@pytest.mark.parametrize("w_one", [True, False])
+def test_codes_are_those_of_the_quotient(M, w_one):
+    """q is e4m3(n / s) for the fp32 n and the returned s, but where n / s is
+    within two fp32 ulps of the middle between two codes. n is known to the bit:
+    the rows are small whole numbers, whose squares add up exactly in any order,
+    K is a power of two, and the inverse root and both products round once."""
+    K = 1024
+    g = torch.Generator(device="cuda").manual_seed(M)
+    x = torch.randint(-100, 101, (M, K), generator=g, device="cuda").to(torch.bfloat16)
+    w = to_dev(synth.uniform_bf16((K,), 0.25, 2.0, seed=41))
+    if w_one:
+        w = torch.ones_like(w)
+    q, s, y, _ = fb.fp8_add_rmsnorm_quant(x, weight=w, eps=0.0)
+    mean = (x.double() ** 2).sum(dim=1, keepdim=True) / K
+    rstd = (1.0 / mean.sqrt()).float()
+    n = (x.float() * rstd) * w.float()
+    assert torch.equal(y, n.to(torch.bfloat16))
+    amax = n.abs().view(M, K // 128, 128).amax(dim=2)
+    assert torch.equal(s, (amax.double() / 448).float())
+    v = n.double() / s.double().repeat_interleave(128, dim=1)
+    got, want = ref.e4m3_values(q), ref.e4m3_round(v)
+    off = got != want
+    middle = (got[off] + want[off]) / 2
+    ulp = torch.exp2(torch.floor(torch.log2(v[off].abs())) - 23)
+    assert bool(((got[off] - want[off]).abs() <= ref.e4m3_step(torch.maximum(got[off].abs(), want[off].abs()))).all())
+    assert bool(((v[off] - middle).abs() <= 2 * ulp).all())
