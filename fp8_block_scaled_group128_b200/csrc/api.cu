@@ -400,7 +400,7 @@ static int add_rmsnorm_quant(const void* x, const void* res, const void* w, floa
   if (int st = current_device_info(&dev)) return st;
   int* err = device_error_word();
   if (err == nullptr) return FP8BS_ERR_CUDA;
-  return from_cuda(launch_add_rmsnorm_quant(x, res, w, eps, M, K, res_out, y, q, s, ue8m0,
+  return from_cuda(launch_add_rmsnorm_quant(x, res, w, eps, M, K, res_out, y, q, s, ue8m0, dev,
                                             wait_limit(), err, static_cast<cudaStream_t>(stream)));
 }
 
@@ -439,7 +439,7 @@ int moe_route_topk(const void* logits, int logits_bf16, const float* bias, int s
   if (int st = current_device_info(&dev)) return st;
   return from_cuda(launch_moe_route(logits, logits_bf16 != 0, bias,
                                     scoring == FP8BS_ROUTE_SIGMOID, M, E, top_k, n_group,
-                                    topk_group, renormalize != 0, scale, ids, weights,
+                                    topk_group, renormalize != 0, scale, ids, weights, dev,
                                     static_cast<cudaStream_t>(stream)));
 }
 

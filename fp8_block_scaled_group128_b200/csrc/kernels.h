@@ -81,16 +81,17 @@ int launch_sparse24_gemm(const void* qa, const float* sa, const void* vals, cons
 // Residual addition, RMS norm and 1x128 quantization (fp32 scales, or UE8M0
 // codes): res, w, res_out and y may be null; res_out may equal x or res.
 constexpr int64_t kNormMaxK = 65536;
+struct DeviceInfo;
 cudaError_t launch_add_rmsnorm_quant(const void* x, const void* res, const void* w, float eps,
                                      int64_t M, int64_t K, void* res_out, void* y, void* q,
-                                     void* s, bool ue8m0, long long wait_limit, int* err,
-                                     cudaStream_t stream);
+                                     void* s, bool ue8m0, const DeviceInfo& dev,
+                                     long long wait_limit, int* err, cudaStream_t stream);
 
 // The router's choice of top_k of E experts per token and their weights.
 cudaError_t launch_moe_route(const void* logits, bool bf16, const float* bias, bool sigmoid,
                              int64_t M, int64_t E, int64_t top_k, int64_t n_group,
                              int64_t topk_group, bool renorm, float scale, int32_t* ids,
-                             float* weights, cudaStream_t stream);
+                             float* weights, const DeviceInfo& dev, cudaStream_t stream);
 
 // The expert MLP of up to kMoeMaxM tokens (moe_mlp.cu).
 constexpr int64_t kMoeMaxM = 128;

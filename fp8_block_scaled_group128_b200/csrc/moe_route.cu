@@ -23,8 +23,7 @@ namespace fp8bs {
 
 namespace {
 
-constexpr int kWarps = 4;         // warps of a block where there are many rows
-constexpr int kFewRows = 592;     // four per SM
+constexpr int kWarps = 4;   // warps of a block where there are many rows
 
 struct RouteArgs {
   const void* logits;
@@ -250,11 +249,11 @@ __global__ void __launch_bounds__(1024) route_kernel(const RouteArgs a) {
 }
 
 template <bool kScore>
-cudaError_t launch_route(const RouteArgs& a, cudaStream_t stream) {
-  // few rows: a thread for each expert (one row of 256: 4.1 us, with a warp 6.9);
+cudaError_t launch_route(const RouteArgs& a, const DeviceInfo& dev, cudaStream_t stream) {
+  // up to four rows an SM: a thread for each expert (one row of 256: 4.1 us, with a warp 6.9);
   // many: one or two warps for a row (4096 rows of 256: 11.1 us with two, 12.2 with
   // one, 13.5 with eight)
-  const bool few = a.M <= kFewRows;
+  const bool few = a.M <= 4 * dev.sm_count;
   const int T = few ? (a.E + 31) / 32 * 32 : a.E > 64 ? 64 : 32;
   const int R = few ? 1 : 32 * kWarps / T;
   const int64_t blocks = (a.M + R - 1) / R;
@@ -262,7 +261,7 @@ cudaError_t launch_route(const RouteArgs& a, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(blocks), 1, 1);
   cfg.blockDim = dim3(static_cast<unsigned>(T), static_cast<unsigned>(R), 1);
-  // at most 4 x 1024 x 8 bytes
+  // at most 2 x 1024 x 8 bytes (four rows have no more than 64 experts)
   cfg.dynamicSmemBytes = (kScore ? 8 : 4) * R * static_cast<size_t>(a.E);
   cfg.stream = stream;
   cudaLaunchAttribute pdl;
@@ -278,7 +277,7 @@ cudaError_t launch_route(const RouteArgs& a, cudaStream_t stream) {
 cudaError_t launch_moe_route(const void* logits, bool bf16, const float* bias, bool sigmoid,
                              int64_t M, int64_t E, int64_t top_k, int64_t n_group,
                              int64_t topk_group, bool renorm, float scale, int32_t* ids,
-                             float* weights, cudaStream_t stream) {
+                             float* weights, const DeviceInfo& dev, cudaStream_t stream) {
   RouteArgs a;
   a.logits = logits;
   a.bias = bias;
@@ -297,8 +296,8 @@ cudaError_t launch_moe_route(const void* logits, bool bf16, const float* bias, b
   while ((2 << a.lg_lanes) * n_group <= 32) ++a.lg_lanes;
   const int per = static_cast<int>(E / n_group);
   a.per_inv = ((1 << 20) + per - 1) / per;   // exact quotients for e < 1024
-  return bias != nullptr || n_group > 1 ? launch_route<true>(a, stream)
-                                        : launch_route<false>(a, stream);
+  return bias != nullptr || n_group > 1 ? launch_route<true>(a, dev, stream)
+                                        : launch_route<false>(a, dev, stream);
 }
 
 }  // namespace fp8bs

@@ -74,8 +74,8 @@ __device__ __forceinline__ float absmax_nan(float a, float b, float c) {
 // (1 + d) / s has |d| <= 2^-23 (one ulp); a Newton step leaves d^2 and one
 // rounding, together below 2^-23.99 relative. A quotient of mantissa m < 2 is then
 // off by m / 2 ulps from 1 / s and half an ulp from the product, below 1.6 in all
-// (without the step m + 1/2, up to 2.5; it costs nothing measurable). For scales whose reciprocal is not a normal number, zero and NaN the IEEE
-// quotients.
+// (without the step m + 1/2, up to 2.5; it costs nothing measurable). For scales
+// whose reciprocal is not a normal number, zero and NaN the IEEE quotients.
 __device__ __forceinline__ uint2 encode8_by_reciprocal(const float (&x)[8], float s) {
   if (!(s >= 7.88860905e-31f)) return encode8f(x, ScaleDivider(s));   // 2^-100
   float inv;
@@ -262,7 +262,6 @@ __global__ void __launch_bounds__(1024) norm_quant_kernel(const NormArgs a) {
 // behind a ring of bulk copies took 59, 19.5 and 27 us.
 constexpr int kRowSmem = 100 * 1024;   // at least two blocks per SM
 constexpr int kRowThreads = 512;
-constexpr int64_t kManyRows = 149;
 
 struct RowArgs {
   NormArgs n;
@@ -443,8 +442,8 @@ cudaError_t launch_norm(const NormArgs& a, cudaStream_t stream) {
 
 cudaError_t launch_add_rmsnorm_quant(const void* x, const void* res, const void* w, float eps,
                                      int64_t M, int64_t K, void* res_out, void* y, void* q,
-                                     void* s, bool ue8m0, long long wait_limit, int* err,
-                                     cudaStream_t stream) {
+                                     void* s, bool ue8m0, const DeviceInfo& dev,
+                                     long long wait_limit, int* err, cudaStream_t stream) {
   NormArgs a;
   a.x = static_cast<const uint4*>(x);
   a.res = static_cast<const uint4*>(res);
@@ -459,10 +458,8 @@ cudaError_t launch_add_rmsnorm_quant(const void* x, const void* res, const void*
   a.eps = eps;
   // more rows than SMs: the rows' latency no longer decides (150 rows of 7168: 4.6 us
   // either way)
-  const bool many = K * (res != nullptr ? 4 : 2) <= kRowSmem && M >= kManyRows;
+  const bool many = K * (res != nullptr ? 4 : 2) <= kRowSmem && M > dev.sm_count;
   if (many) {
-    DeviceInfo dev;
-    if (current_device_info(&dev) != FP8BS_OK) return cudaErrorUnknown;
     const RowArgs rows{a, wait_limit, err};
     if (res != nullptr)
       return ue8m0 ? launch_rows<true, true>(rows, dev, stream)

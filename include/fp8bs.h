@@ -309,8 +309,8 @@ int fp8_gather_columns(const void* src_bf16, int64_t P, int64_t M, int64_t Np, v
  *       no less exact. With eps = 0 a row of zeros gives NaN (0 / 0).
  * The codes come from the fp32 n (not from y). They are those of e4m3(n / s)
  * except where n / s lies within two fp32 ulps of the middle between two codes.
- * M >= 149 takes another kernel than fewer rows: the same row can differ in such
- * a code, and in the last bits of n, between the two.
+ * More rows than the GPU has SMs (148) take another kernel than fewer: the same
+ * row can differ in such a code, and in the last bits of n, between the two.
  * K a positive multiple of 128, at most 65536. A group with an n that is NaN or
  * beyond fp32 gets the scale NaN (UE8M0: code 255). A row with a NaN is NaN
  * throughout; in one with an infinity n is NaN there and 0 elsewhere.
