@@ -8,8 +8,8 @@
 //     d_j  = the block-scaled product of h's codes with expert e's down rows
 //   y[m] = bf16_rn(sum_j weights[m][j] * d_j)
 //
-// Bound: HBM. Every chosen expert's 3 I K weight bytes are read once, whatever
-// the number of its tokens; at the copy bandwidth an SM gets a 128 x 128 tile
+// Bound: HBM, where the experts are wide and not crowded. Every chosen expert's
+// 3 I K weight bytes are read once for up to 64 of its tokens; at the copy bandwidth an SM gets a 128 x 128 tile
 // (16 KB) every ~700 cycles, and both the MMAs and the promotion of a tile
 // take less than that. Measured, the weights' bytes over the time, of the copy
 // bandwidth: 64 tokens on 32 of 256 experts of 7168 x 2048 186 to 206 us (91 to
@@ -21,6 +21,14 @@
 // and in calls below 40 us the way from gate+up over h to down (6 to 10 us).
 // The smallest call takes 12.9 us.
 //
+// Far from that bound: narrow experts, whose down results are one or two units
+// deep, so that a ticket, the hand-over to six readers, the partial sums and a
+// count go with every 16 to 64 KB (16 tokens on 64 experts of 7168 x 128 58 us of
+// 21.4; 64 on 32 of 4096 x 256 44 of 15.4; 8 on 64 of 2048 x 256 30 of 9.6); and few
+// crowded experts, whose lists have less than three chunks for an SM or leave some
+// without any (128 tokens on 2 experts of 4096 x 1536 31 us of 5.8, 64 on 4 of
+// 3584 x 2560 42 of 16.8).
+//
 // Two launches, chained by programmatic dependent launch:
 //
 //   moe_plan_kernel  one block: the chosen experts in order, each with its
@@ -28,9 +36,11 @@
 //   moe_mlp_kernel   one CTA per SM: gate+up and down
 //
 // Both products put 128 weight rows on the MMA's M side and tokens on its N
-// side: the rows of one expert, in blocks of at most 64 (an expert with more is
-// walked twice; its weights then come from L2 the second time). The work is a
-// list of chunks: some K-blocks of one result (gate+up: expert and 128
+// side: the rows of one expert, in blocks of at most 64. An expert with more is
+// walked twice, all of one product's weights for the first block before the second:
+// the second time they come from L2 where they fit (128 tokens on one expert of
+// 7168 x 2048: 45.1 MB from HBM for 44.0 MB of weights), else from HBM again (of
+// 7168 x 9216: 372 for 198 MB). The work is a list of chunks: some K-blocks of one result (gate+up: expert and 128
 // intermediate columns; down: expert and 128 output columns). A CTA claims the
 // next chunk from a counter, streams its weights, writes the chunk's fp32
 // partial sums to the workspace and goes on; nothing in that stream waits for

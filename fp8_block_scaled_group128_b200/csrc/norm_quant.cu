@@ -13,8 +13,9 @@
 //
 // Bound: HBM; a row is read once. Few rows are held in registers (as bf16)
 // between the sum of squares and the codes, with as many threads as a row has
-// chunks: one row of 4096 2.1 us, 64 rows of 7168 3.2 us. Many rows go through
-// shared memory (norm_row_kernel).
+// chunks: one row of 4096 2.1 us, 64 rows of 7168 3.3 us (in a graph). Rows above
+// 32768 keep eight chunks a thread and spill some (16 rows of 65536 16.7 us). Many
+// rows go through shared memory (norm_row_kernel).
 #include <mutex>
 
 #include "common.cuh"
@@ -255,10 +256,10 @@ __global__ void __launch_bounds__(1024) norm_quant_kernel(const NormArgs a) {
 // makes the codes. A thread's registers hold one 16-byte chunk at a time, so
 // that enough blocks are resident to keep HBM busy while others compute.
 //
-// 8192 rows of 4096 with residual and y: 49.3 us, 93% of the copy bandwidth (in
-// registers: 53.7); 1037 rows of 14336, codes only: 15.6 us (in registers: 24.2),
-// bound by instructions there, about 20 for an element; 2048 rows of 7168: 26.0
-// (30.9). A persistent kernel whose teams of warps held their rows in registers
+// 8192 rows of 4096 with residual and y: 49.3 to 50.6 us, 92 to 93% of the copy
+// bandwidth (in registers: 53.7), 47.2 in a graph (UE8M0 47.4); 1037 rows of 14336,
+// codes only: 15.4 us (in registers: 24.2; UE8M0 14.8), bound by instructions
+// there, 22 for an element; 2048 rows of 7168: 24.5 in a graph. A persistent kernel whose teams of warps held their rows in registers
 // behind a ring of bulk copies took 59, 19.5 and 27 us.
 constexpr int kRowSmem = 100 * 1024;   // at least two blocks per SM
 constexpr int kRowThreads = 512;

@@ -359,7 +359,9 @@ int moe_route_topk(const void* logits, int logits_bf16, const float* bias, int s
 /*
  * The whole expert MLP of a mixture-of-experts layer for a few tokens (decode):
  * gate+up, SwiGLU, quantization, down, and the weighted sum over a token's
- * experts. For more tokens group the rows by expert and use fp8_grouped_gemm.
+ * experts. More than 128 tokens are refused: fp8_grouped_gemm has the products
+ * then, but the grouping of the rows by expert, the SwiGLU between the two products
+ * and the weighted sum are the caller's.
  *
  *   for token m and choice j with expert e = ids[m][j] - first_expert:
  *     g, u = the block-scaled products (as fp8_block_gemm, in fp32) of qa[m]
@@ -378,14 +380,20 @@ int moe_route_topk(const void* logits, int logits_bf16, const float* bias, int s
  *   y_bf16 [M][K], output; it and the workspace overlap no operand.
  *   workspace: at least fp8bs_moe_workspace_bytes(M, K, I, E, top_k) bytes, 16-byte
  *       aligned; its contents need no preparation and mean nothing afterwards. The
- *       size never falls with M, so that one workspace serves fewer tokens too.
+ *       size never falls with M, so that one workspace serves fewer tokens too. It
+ *       is mostly fp32 partial sums, up to 32 MiB for each product and more only
+ *       where a single set takes more: 17 to 71 MB for 1 to 128 tokens with 2
+ *       choices of 4096 x 14336 (K x I) or 8 of 7168 x 2048, 650 MB for 128 tokens
+ *       with 32 choices of 7168 x 14336.
  *       Calls that can run at the same time need workspaces of their own.
  *   0 <= M <= 128, 1 <= E <= 1024, 1 <= top_k <= 32, first_expert >= 0; K and I
  *   positive multiples of 128.
  * The _ue8m0 form takes all scales as UE8M0 codes (255: NaN) and quantizes h with
  * them.
  * A row whose h is not finite somewhere (NaN, or beyond fp32) gives NaN.
- * Results are deterministic: the same inputs give the same bytes every call.
+ * Results are deterministic: the same inputs give the same bytes every call. How
+ * the sums are cut goes by the whole call: a token's row can differ in its rounding
+ * from that of a call with other tokens.
  */
 int fp8_moe_mlp(const void* qa, const float* sa, const int32_t* ids, const float* weights,
                 const void* qw_gate_up, const float* sw_gate_up, const void* qw_down,
