@@ -257,10 +257,11 @@ __global__ void __launch_bounds__(1024) norm_quant_kernel(const NormArgs a) {
 // that enough blocks are resident to keep HBM busy while others compute.
 //
 // 8192 rows of 4096 with residual and y: 49.3 to 50.6 us, 92 to 93% of the copy
-// bandwidth (in registers: 53.7), 47.2 in a graph (UE8M0 47.4); 1037 rows of 14336,
-// codes only: 15.4 us (in registers: 24.2; UE8M0 14.8), bound by instructions
-// there, 22 for an element; 2048 rows of 7168: 24.5 in a graph. A persistent kernel whose teams of warps held their rows in registers
-// behind a ring of bulk copies took 59, 19.5 and 27 us.
+// bandwidth (in registers: 53.7), 47.2 in a graph (UE8M0 47.4); 1037 rows of
+// 14336, codes only: 15.4 us (in registers: 24.2; UE8M0 14.8), bound by
+// instructions there, 22 for an element; 2048 rows of 7168: 24.5 in a graph. A
+// persistent kernel whose teams of warps held their rows in registers behind a
+// ring of bulk copies took 59, 19.5 and 27 us.
 constexpr int kRowSmem = 100 * 1024;   // at least two blocks per SM
 constexpr int kRowThreads = 512;
 
